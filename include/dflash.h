@@ -60,7 +60,7 @@ enum dflash_status {
   DFLASH_EBOUNDS = -5,    /* a device bounds check failed (builds with DFL_DEBUG_CHECKS; see below) */
 };
 
-enum dflash_dtype { DFLASH_F32 = 0, DFLASH_BF16 = 1, DFLASH_Q4G64 = 2 };
+enum dflash_dtype { DFLASH_F32 = 0, DFLASH_BF16 = 1, DFLASH_Q4G64 = 2, DFLASH_F16 = 3 /* rows of the calls on a dflash_cache */ };
 enum dflash_ffn { DFLASH_FFN_SWIGLU = 0, DFLASH_FFN_GELU = 1 };
 
 typedef struct {
@@ -329,6 +329,147 @@ int dflash_rows_matmul(dflash_handle* h, int matrix, int layer, int n_rows, cons
                        int ldx, float* y, int ldy, void* scratch, size_t scratch_bytes, void* stream);
 
 void dflash_destroy(dflash_handle* h);
+
+/* ---- paged 8-bit context cache -----------------------------------------------------------------
+ * Context K/V rows in 8 bits, in blocks of block_tokens tokens that all requests share. The dflash.ts
+ * page keeps every request's context rows whole ("projectContextRows"); here a request's rows live in
+ * the blocks that its row of a block table names, so memory follows the lengths that requests have
+ * and not the longest one allowed, at half the bytes of the f16 ring. Three kinds of call:
+ *   dflash_pool_reserve / dflash_pool_truncate   block tables and slots, built on the GPU from the
+ *                          requests' lengths; blocks come from and go back to a stack of free ones
+ *   dflash_cache_append    new K/V rows quantised into their slots
+ *   dflash_cache_attention softmax attention of a few rows per request over the cached rows
+ *
+ * Storage. A code is an e4m3 byte and stands for code * scale, with one fp32 scale for each (layer,
+ * block, KV head) of K and of V. Codes of (layer l, block n, head h, token t, column c) are at byte
+ * l * layer_stride + n * block_stride + h * head_stride + t * token_stride + c of k and of v; every
+ * stride and both addresses are multiples of 16. Scales are [n_layers][n_blocks][n_kv_heads].
+ * Position p of a request is token p % T of block table[request][(p / T) % table_blocks], T =
+ * block_tokens; its slot is block * T + p % T. The modulo makes the table a ring (dflash_pool.ring). */
+typedef struct {
+  void *k, *v;               /* codes, see above; owned by the caller, as the scales */
+  float *k_scale, *v_scale;
+  int n_layers, n_blocks;    /* n_blocks * block_tokens < 2^31 */
+  int block_tokens;          /* T: 16, 32, 64 or 128 */
+  int n_kv_heads, head_dim;  /* head_dim in {64, 128, 256} */
+  int64_t layer_stride, block_stride, head_stride, token_stride;   /* bytes */
+  /* limits of the attention calls (all 0: none are made) */
+  int n_q_heads;             /* a multiple of n_kv_heads */
+  int max_requests;          /* requests per call, <= DFLASH_CACHE_MAX_REQUESTS */
+  int max_q;                 /* query rows per request, <= DFLASH_CACHE_MAX_Q */
+} dflash_cache_config;
+#define DFLASH_CACHE_MAX_REQUESTS 1024
+#define DFLASH_CACHE_MAX_Q 128
+
+typedef struct dflash_cache dflash_cache;
+
+/* Rows in caller memory: element (layer, row, head, column) at data + layer * layer_stride + row *
+ * row_stride + head * head_stride + column, strides in elements. data is 16-byte aligned and the
+ * strides are multiples of 16 bytes. */
+typedef struct {
+  const void* data;
+  int64_t layer_stride, row_stride, head_stride;
+} dflash_rows;
+
+/* Bytes of device workspace dflash_cache_create needs (0 if cfg is invalid). */
+size_t dflash_cache_workspace_bytes(const dflash_cache_config* cfg);
+
+/* A host-side handle over the caller's codes and scales and a caller-owned workspace (device memory,
+ * 256-byte aligned, >= dflash_cache_workspace_bytes; its error word is zeroed on `stream`). Codes and
+ * scales are not touched. The handle belongs to the device current at create; its calls check that
+ * this device is current (DFLASH_EINVAL) and are issued in order on one stream, or on streams that
+ * the caller orders: attention calls share the workspace. */
+int dflash_cache_create(const dflash_cache_config* cfg, void* workspace, size_t workspace_bytes, void* stream,
+                        dflash_cache** out);
+void dflash_cache_destroy(dflash_cache* c);
+
+/* As dflash_check_errors, for the calls on this cache: synchronises `stream`, reads and clears the
+ * error word. DFLASH_ETIMEOUT: a bounded wait gave up, the outputs of that call are undefined.
+ * DFLASH_EBOUNDS (builds with DFL_DEBUG_CHECKS): a slot, block number or row index was out of range;
+ * every build skips such rows and keys. */
+int dflash_cache_check_errors(dflash_cache* c, void* stream);
+
+/* Block tables over a pool of n_blocks blocks; plain host struct, all pointers device memory. */
+typedef struct {
+  int block_tokens;          /* T: 16, 32, 64 or 128 */
+  int n_blocks;              /* entries of free_list */
+  int table_rows, table_blocks;
+  int ring;                  /* 0: a request holds at most table_blocks blocks. 1: it may grow without
+                                end, position p reusing the block of position p - table_blocks * T;
+                                for windowed attention table_blocks >= ceil(window / T) + 1 */
+  int32_t* lens;             /* [table_rows] tokens each request has */
+  int32_t* table;            /* [table_rows][table_blocks] */
+  int32_t* free_list;        /* [n_blocks]: free_count[0] unused blocks, taken from the end */
+  int32_t* free_count;
+  void* scratch;             /* DFLASH_POOL_SCRATCH bytes, zeroed before the first call */
+} dflash_pool;
+#define DFLASH_POOL_SCRATCH 256
+#define DFLASH_POOL_MAX_REQUESTS 1024
+#define DFLASH_POOL_MAX_NEW (1 << 20)   /* tokens reserved per request and call */
+
+/* Reserve n_new[i] more tokens for request i of the call, whose table row is requests[i] (requests
+ * NULL: row i). In the order of the call, a request takes ceil((len + n) / T) - ceil(len / T) blocks
+ * from the end of the free list (a ring stops at table_blocks). granted[i] = 1 if its table row holds
+ * them and the blocks needed by requests 0..i together are free (or it needs none); otherwise 0, and
+ * the request is left as it is with no rows. A request named twice is granted the first time only;
+ * a row number out of range, a negative n_new or one above DFLASH_POOL_MAX_NEW counts as not granted.
+ * row_start int32 [n_requests + 1]: rows before each request, in total. slots int32 [n_slots]: the
+ * slot of every granted row, request by request; -1 behind the last row and for rows that a ring
+ * overwrites within this call. Rows beyond n_slots have no slot: n_slots >= the sum of n_new.
+ * Lens, table and free_count are updated. Calls on one pool are issued in order. */
+int dflash_pool_reserve(const dflash_pool* p, int n_requests, const int32_t* requests, const int32_t* n_new,
+                        int32_t* slots, int n_slots, int32_t* row_start, int32_t* granted, void* stream);
+
+/* Shorten requests to new_len[i] tokens (no effect where they are not longer) and give the blocks
+ * behind it back, such that reserving the same tokens again takes the same blocks. Table entries of
+ * released blocks become -1. The rejected rows of a verified block and finished requests (new_len 0)
+ * are released this way. */
+int dflash_pool_truncate(const dflash_pool* p, int n_requests, const int32_t* requests, const int32_t* new_len,
+                         void* stream);
+
+/* Quantise n_rows K/V rows into their slots (int32 [n_rows], device; negative: the row is skipped),
+ * for layers layer .. layer + n_layers - 1. k, v: rows of `dtype` (DFLASH_F32, DFLASH_BF16 or
+ * DFLASH_F16), indexed by layer - first layer, row and KV head.
+ * The rows of one block stand together in the call, as dflash_pool_reserve orders them. Per layer,
+ * block, head and side: amax = the largest finite magnitude of the block's new rows, s = the smallest
+ * power of two >= 2^-64 with amax <= 448 s. If the block's token 0 is among the rows the block starts
+ * anew with scale s, else its scale becomes max(old, s) and codes that stay are rounded to it. A code
+ * is value / scale rounded to nearest even; infinities saturate, a NaN stays one. Of rows with the
+ * same slot the last one counts. */
+int dflash_cache_append(dflash_cache* c, int layer, int n_layers, int n_rows, const int32_t* slots,
+                        const dflash_rows* k, const dflash_rows* v, int dtype, void* stream);
+
+/* out[row][head] = sum_j softmax_j(scale * q[row][head] . k_j) v_j for the rows of n_requests requests.
+ * Query head h reads KV head h / (n_q_heads / n_kv_heads). */
+typedef struct {
+  int layer, n_requests;
+  int n_rows;                /* query rows of the call; rows behind the last request are left as they are */
+  int max_q;                 /* rows per request: each has max_q (row_start NULL) or at most max_q */
+  int table_rows, table_blocks;
+  const int32_t* requests;   /* device [n_requests]: their rows of lens and table; NULL: 0 .. n_requests - 1 */
+  const int32_t* lens;       /* device: cached tokens of each request */
+  const int32_t* table;      /* device [table_rows][table_blocks] */
+  const int32_t* row_start;  /* device [n_requests + 1] or NULL */
+  int dtype;                 /* DFLASH_BF16 or DFLASH_F16: q, out, k_own, v_own */
+  dflash_rows q;             /* [row][query head][head_dim]; layer_stride is not used */
+  dflash_rows out;
+  dflash_rows k_own, v_own;  /* [row][KV head][head_dim], data NULL: none. The rows' own K/V, not cached
+                                (the drafted block of Eq 3): row i attends over the cached rows and
+                                the own rows of its request */
+  int causal;                /* 0: every row sees all of them. 1: row i of a request stands at position
+                                len + i (own rows) or len - n + i (the n rows are the last cached ones)
+                                and sees its own position and those before it */
+  int window;                /* 0: everything. causal: the row's last `window` positions, its own
+                                included; else the last `window` cached rows (and every own row) */
+  float scale;
+} dflash_attention;
+
+/* Rows that see no key get zeros. Keys whose table entry is out of range are not seen. Masked keys are
+ * never read, whatever their blocks hold. Rounding: queries and probabilities enter the tensor
+ * cores as sums of e4m3 values, 8 significant bits for bf16 rows and 11 for f16 rows (the format's own
+ * precision); products accumulate in fp32, softmax sums and outputs are fp32 and rounded once. */
+int dflash_cache_attention(dflash_cache* c, const dflash_attention* a, void* stream);
+
 
 /* Allocation-free greedy token and softmax confidence for logits the caller already holds.
  * The pages describe no such call; it exists for callers that cannot allocate device memory on

@@ -26,14 +26,14 @@ LIB_PATH_DEBUG = os.path.join(_BUILD_DEBUG, "libdflash.so")
 def _debug_selected() -> bool:
     return os.environ.get("DFLASH_DEBUG_CHECKS") == "1"
 _SOURCES = ["abi.cu", "gemv_q4.cu", "gemv_bf16.cu", "gemv_f32.cu", "attn.cu", "misc.cu", "noalloc.cu", "gemm_tc05.cu", "tc05_epi.cu",
-            "proj_tc05.cu"]
-_HEADERS = ["internal.h", "common.cuh", "gemv_impl.cuh", "gemm_tc05.h", "tc05.cuh"]
+            "proj_tc05.cu", "pool.cu", "cache_append.cu", "cache_attn.cu", "cache_abi.cu"]
+_HEADERS = ["internal.h", "common.cuh", "gemv_impl.cuh", "gemm_tc05.h", "tc05.cuh", "cache.h"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-gencode", "arch=compute_103a,code=sm_103a",
               "-Xcompiler", "-fPIC"]
 
 DFLASH_OK, DFLASH_DECLINED, DFLASH_EINVAL, DFLASH_ECAPACITY, DFLASH_ECUDA, DFLASH_ETIMEOUT = 0, 1, -1, -2, -3, -4
 DFLASH_EBOUNDS = -5
-DFLASH_F32, DFLASH_BF16, DFLASH_Q4G64 = 0, 1, 2
+DFLASH_F32, DFLASH_BF16, DFLASH_Q4G64, DFLASH_F16 = 0, 1, 2, 3
 DFLASH_MAX_LAYERS = 8
 DFLASH_MAX_BATCH = 64
 DFLASH_NOALLOC_MAX_ROWS = 64
@@ -123,13 +123,41 @@ DFLASH_ROWS_MATMUL_MAX = 160
 DFLASH_MAT_CTX, DFLASH_MAT_QKV, DFLASH_MAT_O, DFLASH_MAT_GATEUP, DFLASH_MAT_DOWN, DFLASH_MAT_LM = range(6)
 
 
+class dflash_cache_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + \
+               [(n, ctypes.c_int) for n in ("n_layers", "n_blocks", "block_tokens", "n_kv_heads", "head_dim")] + \
+               [(n, ctypes.c_int64) for n in ("layer_stride", "block_stride", "head_stride", "token_stride")] + \
+               [(n, ctypes.c_int) for n in ("n_q_heads", "max_requests", "max_q")]
+
+
+class dflash_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("layer_stride", "row_stride", "head_stride")]
+
+
+class dflash_pool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("block_tokens", "n_blocks", "table_rows", "table_blocks", "ring")] + \
+               [(n, ctypes.c_void_p) for n in ("lens", "table", "free_list", "free_count", "scratch")]
+
+
+class dflash_attention(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("layer", "n_requests", "n_rows", "max_q", "table_rows", "table_blocks")] + \
+               [(n, ctypes.c_void_p) for n in ("requests", "lens", "table", "row_start")] + [("dtype", ctypes.c_int)] + \
+               [(n, dflash_rows) for n in ("q", "out", "k_own", "v_own")] + \
+               [("causal", ctypes.c_int), ("window", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+DFLASH_CACHE_MAX_REQUESTS, DFLASH_CACHE_MAX_Q = 1024, 128
+DFLASH_POOL_SCRATCH, DFLASH_POOL_MAX_REQUESTS, DFLASH_POOL_MAX_NEW = 256, 1024, 1 << 20
+
 _lib = None
 SYMBOLS = ["dflash_workspace_bytes", "dflash_create", "dflash_project_ctx", "dflash_draft_block",
            "dflash_accept", "dflash_reset_request", "dflash_ctx_len", "dflash_check_errors",
            "dflash_get_stats", "dflash_set_probe", "dflash_launch_count", "dflash_destroy",
            "dflash_status_str", "dflash_greedy_from_logits_noalloc", "dflash_draft_lengths",
            "dflash_accept_kept", "dflash_rows_matmul_plan", "dflash_rows_matmul", "dflash_set_wait_limit",
-           "dflash_debug_stall", "dflash_accept_histogram"]
+           "dflash_debug_stall", "dflash_accept_histogram", "dflash_cache_workspace_bytes", "dflash_cache_create",
+           "dflash_cache_destroy", "dflash_cache_check_errors", "dflash_pool_reserve", "dflash_pool_truncate",
+           "dflash_cache_append", "dflash_cache_attention"]
 
 
 def lib():
@@ -184,6 +212,22 @@ def lib():
         L.dflash_debug_stall.argtypes = [vp, i32]
         L.dflash_accept_histogram.restype = i32
         L.dflash_accept_histogram.argtypes = [vp, P(ctypes.c_uint64), i32, vp]
+        L.dflash_cache_workspace_bytes.restype = ctypes.c_size_t
+        L.dflash_cache_workspace_bytes.argtypes = [P(dflash_cache_config)]
+        L.dflash_cache_create.restype = i32
+        L.dflash_cache_create.argtypes = [P(dflash_cache_config), vp, ctypes.c_size_t, vp, P(vp)]
+        L.dflash_cache_destroy.restype = None
+        L.dflash_cache_destroy.argtypes = [vp]
+        L.dflash_cache_check_errors.restype = i32
+        L.dflash_cache_check_errors.argtypes = [vp, vp]
+        L.dflash_pool_reserve.restype = i32
+        L.dflash_pool_reserve.argtypes = [P(dflash_pool), i32, vp, vp, vp, i32, vp, vp, vp]
+        L.dflash_pool_truncate.restype = i32
+        L.dflash_pool_truncate.argtypes = [P(dflash_pool), i32, vp, vp, vp]
+        L.dflash_cache_append.restype = i32
+        L.dflash_cache_append.argtypes = [vp, i32, i32, i32, vp, P(dflash_rows), P(dflash_rows), i32, vp]
+        L.dflash_cache_attention.restype = i32
+        L.dflash_cache_attention.argtypes = [vp, P(dflash_attention), vp]
         _lib = L
     return _lib
 
@@ -391,3 +435,6 @@ class Handle:
             self.close()
         except Exception:
             pass
+
+
+from .cache import BlockPool, Cache  # noqa: E402,F401  (the binding of the paged context cache uses the names above)
