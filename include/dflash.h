@@ -464,8 +464,10 @@ typedef struct {
   float scale;
 } dflash_attention;
 
-/* Rows that see no key get zeros. Keys whose table entry is out of range are not seen. Masked keys are
- * never read, whatever their blocks hold. Rounding: queries and probabilities enter the tensor
+/* Rows that see no key get zeros. Keys whose table entry is out of range are not seen, nor are those that
+ * a ring no longer holds (before len - table_blocks * T). What masked keys' blocks hold does not matter; a
+ * NaN in a value that some rows of a request see and others do not makes the whole output row of those
+ * that see it NaN. Rounding: queries and probabilities enter the tensor
  * cores as sums of e4m3 values, 8 significant bits for bf16 rows and 11 for f16 rows (the format's own
  * precision); products accumulate in fp32, softmax sums and outputs are fp32 and rounded once. */
 int dflash_cache_attention(dflash_cache* c, const dflash_attention* a, void* stream);

@@ -389,26 +389,6 @@ bool disabled_by_env() {
   return v && v[0] == '1';
 }
 
-typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled tensor_map_encoder() {
-  static std::atomic<EncodeTiled> encode{nullptr};
-  EncodeTiled e = encode.load(std::memory_order_acquire);
-  if (!e) {
-    cudaDriverEntryPointQueryResult q;
-    void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !fn)
-      return nullptr;
-    e = reinterpret_cast<EncodeTiled>(fn);
-    encode.store(e, std::memory_order_release);
-  }
-  return e;
-}
-
 // f16 activation rows [rows][ld] as 2-D tiles of 64 inputs x box_rows rows in the 128-byte
 // swizzle (the K-major operand layout of the tcgen05 MMA); rows past `rows` read as zero.
 int make_rows_map(const void* base, int k, int rows, int ld, int box_rows, CUtensorMap* map) {

@@ -27,11 +27,19 @@ struct CacheAppendArgs {
 
 cudaError_t launch_cache_append(int dtype, const CacheAppendArgs& a, cudaStream_t s);
 
+// How a call's query rows are laid out over CTAs (plan_cache_attn): the grp * n rows of one request and
+// KV head are cut into chunks of rc rows, each padded to rp columns and carried as `terms` e4m3 terms.
+struct CacheAttnPlan {
+  int terms;               // e4m3 terms of a query or probability: 2 (bf16), 3 (f16)
+  int chunks, rc, rp, n;   // n: MMA columns, terms * rp rounded up to 16 (<= 128)
+  int ctas_per_sm, stages, tmem_cols;
+  size_t smem;
+};
+CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req);
+
 struct CacheAttnArgs {
-  const uint8_t *k, *v;
   const float *k_scale, *v_scale;                  // of the call's layer
-  int64_t c_block, c_head, c_token;
-  int n_blocks, n_kv, hd, log_t, grp;
+  int layer, n_blocks, n_kv, hd, log_t, grp;
   int n_req, n_rows, max_q, table_rows, table_blocks, causal, window;
   const int32_t *requests, *lens, *table, *row_start;
   const void *q, *k_own, *v_own;
@@ -39,8 +47,14 @@ struct CacheAttnArgs {
   int64_t q_row, q_head, o_row, o_head, ko_row, ko_head, vo_row, vo_head;   // elements
   float scale_log2;                                // scale * log2(e)
   unsigned* err;
+  CacheAttnPlan p;
+  int grid;                                        // CTAs of the first kernel
+  int* units;                                      // [n_req + 1] key tiles before each request
+  float* part_o;                                   // [grid + n_req * n_kv * chunks][rp][hd]
+  float2* part_ml;                                 // [..][rp] (reference, sum)
 };
 
-cudaError_t launch_cache_attn(int dtype, const CacheAttnArgs& a, cudaStream_t s);
+cudaError_t launch_cache_attn(int dtype, const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                              cudaStream_t s);
 
 }  // namespace dfl

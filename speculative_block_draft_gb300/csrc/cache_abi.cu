@@ -2,6 +2,7 @@
 // host-side handle. The kernels are in cache_append.cu and cache_attn.cu, the block tables in pool.cu.
 #include <math.h>
 
+#include <algorithm>
 #include <new>
 
 #include "cache.h"
@@ -12,6 +13,12 @@ struct dflash_cache {
   dflash_cache_config cfg;
   int device = 0, log_t = 0;
   unsigned* err = nullptr;      // [0] error bits, [1] wait limit in us (0: 1 s)
+  int n_sm = 148;
+  int* units = nullptr;         // [max_requests + 1]
+  float2* part_ml = nullptr;    // attention pieces: rows of (reference, sum), then of head_dim floats
+  float* part_o = nullptr;
+  int64_t part_rows = 0;
+  CUtensorMap kmap{}, vmap{};
 };
 
 namespace {
@@ -26,7 +33,9 @@ bool valid(const dflash_cache_config* c) {
   if (c->n_kv_heads < 1 || c->n_kv_heads > 4096) return false;
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return false;
   if (!aligned_16(c->k) || !aligned_16(c->v)) return false;
-  if (c->layer_stride < 0 || c->block_stride < 0 || c->head_stride < 0 || c->token_stride < c->head_dim) return false;
+  if (c->layer_stride < (c->n_layers > 1) || c->block_stride < (c->n_blocks > 1) || c->head_stride < (c->n_kv_heads > 1) ||
+      c->token_stride < c->head_dim)
+    return false;
   if (!multiple_of_16(c->layer_stride) || !multiple_of_16(c->block_stride) || !multiple_of_16(c->head_stride) ||
       !multiple_of_16(c->token_stride))
     return false;
@@ -37,6 +46,50 @@ bool valid(const dflash_cache_config* c) {
   if (c->n_q_heads == 0 && c->max_requests == 0 && c->max_q == 0) return true;
   return c->n_q_heads >= 1 && c->n_q_heads <= 65535 && c->n_q_heads % c->n_kv_heads == 0 && c->max_requests >= 1 &&
          c->max_requests <= DFLASH_CACHE_MAX_REQUESTS && c->max_q >= 1 && c->max_q <= DFLASH_CACHE_MAX_Q;
+}
+
+// Rows of attention pieces that a call within the limits can leave: one per query row, padded, of each
+// (request, KV head), and the CTAs' own. A chunk of rows is padded to less than 8 + 1 more, and there are at
+// least 40 rows in every chunk but one; a CTA's chunk holds at most 64 rows, and an SM two CTAs.
+int64_t piece_rows(const dflash_cache_config& f, int n_sm) {
+  const int64_t rows = (int64_t)(f.n_q_heads / f.n_kv_heads) * f.max_q;
+  return (int64_t)2 * n_sm * 64 + (int64_t)f.max_requests * f.n_kv_heads * (rows + 9 * ((rows + 39) / 40));
+}
+
+size_t round_256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Workspace: error word | units | (m, L) of the pieces | O of the pieces.
+size_t carve(dflash_cache* c, uint8_t* base) {
+  const dflash_cache_config& f = c->cfg;
+  size_t at = 256;
+  c->err = reinterpret_cast<unsigned*>(base);
+  if (f.max_requests) {
+    c->part_rows = piece_rows(f, c->n_sm);
+    c->units = reinterpret_cast<int*>(base + at);
+    at += round_256(4 * (size_t)(f.max_requests + 1));
+    c->part_ml = reinterpret_cast<float2*>(base + at);
+    at += round_256(8 * (size_t)c->part_rows);
+    c->part_o = reinterpret_cast<float*>(base + at);
+    at += round_256(4 * (size_t)c->part_rows * f.head_dim);
+  }
+  return at;
+}
+
+// Codes as [layer][block][head][token][column]; one copy brings the tokens of a block and head, 128 columns (64
+// for head_dim 64) wide, in the swizzle that the MMA reads.
+int make_code_map(const dflash_cache_config& f, void* base, CUtensorMap* map) {
+  EncodeTiled encode = tensor_map_encoder();
+  if (!encode) return DFLASH_ECUDA;
+  const cuuint64_t dims[5] = {(cuuint64_t)f.head_dim, (cuuint64_t)f.block_tokens, (cuuint64_t)f.n_kv_heads, (cuuint64_t)f.n_blocks,
+                              (cuuint64_t)f.n_layers};
+  auto stride = [](int64_t s) { return (cuuint64_t)(s > 0 ? s : 16); };   // 0 only where there is one of it
+  const cuuint64_t strides[4] = {stride(f.token_stride), stride(f.head_stride), stride(f.block_stride), stride(f.layer_stride)};
+  const cuuint32_t box[5] = {(cuuint32_t)(f.head_dim < 128 ? f.head_dim : 128), (cuuint32_t)f.block_tokens, 1, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            f.head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DFLASH_OK : DFLASH_EINVAL;
 }
 
 bool on_device(const dflash_cache* c) {
@@ -56,7 +109,14 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? DFLASH_OK : DFLASH_ECUD
 
 extern "C" {
 
-size_t dflash_cache_workspace_bytes(const dflash_cache_config* cfg) { return valid(cfg) ? 256 : 0; }
+size_t dflash_cache_workspace_bytes(const dflash_cache_config* cfg) {
+  if (!valid(cfg)) return 0;
+  dflash_cache c;
+  c.cfg = *cfg;
+  int dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&c.n_sm, cudaDevAttrMultiProcessorCount, dev);
+  return carve(&c, nullptr);
+}
 
 int dflash_cache_create(const dflash_cache_config* cfg, void* workspace, size_t workspace_bytes, void* stream,
                         dflash_cache** out) {
@@ -68,11 +128,21 @@ int dflash_cache_create(const dflash_cache_config* cfg, void* workspace, size_t 
   if (!c) return DFLASH_EINVAL;
   c->cfg = *cfg;
   while ((1 << c->log_t) < cfg->block_tokens) c->log_t++;
-  c->err = static_cast<unsigned*>(workspace);
+  int st = DFLASH_OK;
   if (cudaGetDevice(&c->device) != cudaSuccess ||
-      cudaMemsetAsync(workspace, 0, 256, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+      cudaDeviceGetAttribute(&c->n_sm, cudaDevAttrMultiProcessorCount, c->device) != cudaSuccess)
+    st = DFLASH_ECUDA;
+  if (st == DFLASH_OK) {
+    carve(c, static_cast<uint8_t*>(workspace));
+    if (cfg->max_requests) {
+      st = make_code_map(*cfg, cfg->k, &c->kmap);
+      if (st == DFLASH_OK) st = make_code_map(*cfg, cfg->v, &c->vmap);
+    }
+  }
+  if (st == DFLASH_OK && cudaMemsetAsync(c->err, 0, 256, static_cast<cudaStream_t>(stream)) != cudaSuccess) st = DFLASH_ECUDA;
+  if (st != DFLASH_OK) {
     delete c;
-    return DFLASH_ECUDA;
+    return st;
   }
   *out = c;
   return DFLASH_OK;
@@ -147,14 +217,10 @@ int dflash_cache_attention(dflash_cache* c, const dflash_attention* p, void* str
   if (p->k_own.data && (!rows_ok(p->k_own, 2) || !rows_ok(p->v_own, 2))) return DFLASH_EINVAL;
   if (!on_device(c)) return DFLASH_EINVAL;
   CacheAttnArgs a{};
-  a.k = static_cast<const uint8_t*>(f.k) + p->layer * f.layer_stride;
-  a.v = static_cast<const uint8_t*>(f.v) + p->layer * f.layer_stride;
   const int64_t scales = (int64_t)p->layer * f.n_blocks * f.n_kv_heads;
   a.k_scale = f.k_scale + scales;
   a.v_scale = f.v_scale + scales;
-  a.c_block = f.block_stride;
-  a.c_head = f.head_stride;
-  a.c_token = f.token_stride;
+  a.layer = p->layer;
   a.n_blocks = f.n_blocks;
   a.n_kv = f.n_kv_heads;
   a.hd = f.head_dim;
@@ -185,7 +251,17 @@ int dflash_cache_attention(dflash_cache* c, const dflash_attention* p, void* str
   a.vo_head = p->v_own.head_stride;
   a.scale_log2 = p->scale * 1.4426950408889634f;
   a.err = c->err;
-  return status_of(launch_cache_attn(p->dtype, a, static_cast<cudaStream_t>(stream)));
+  a.p = plan_cache_attn(p->dtype, f.head_dim, a.grp, p->max_q, p->n_requests);
+  // key tiles are counted in 32 bits: a request has at most as many as its table row names, and one more
+  const int64_t pairs = (int64_t)p->n_requests * f.n_kv_heads * a.p.chunks;
+  const int64_t tiles = pairs * ((((int64_t)p->table_blocks << c->log_t) + 127) / 128 + 1);
+  if (tiles >= (1LL << 31)) return DFLASH_EINVAL;
+  a.grid = (int)std::min<int64_t>((int64_t)a.p.ctas_per_sm * c->n_sm, tiles);
+  if ((a.grid + pairs) * a.p.rp > c->part_rows) return DFLASH_ECAPACITY;
+  a.units = c->units;
+  a.part_o = c->part_o;
+  a.part_ml = c->part_ml;
+  return status_of(launch_cache_attn(p->dtype, a, c->kmap, c->vmap, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -29,14 +29,14 @@ struct Row8;   // 8 consecutive elements of a row, as fp32
 template <>
 struct Row8<float> {
   __device__ static void load(const float* p, float (&x)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
 };
 template <>
 struct Row8<__nv_bfloat16> {
   __device__ static void load(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
     const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -48,7 +48,7 @@ struct Row8<__nv_bfloat16> {
 template <>
 struct Row8<__half> {
   __device__ static void load(const __half* p, float (&x)[8]) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
     const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
   pdl_wait();
   // rows of a block out of range are skipped like negative slots
   auto block_at = [&](int row) {
-    const int s = __ldg(a.slots + row);
+    const int s = a.slots[row];
     const int b = s < 0 ? -1 : s >> a.log_t;
     if (s >= 0 && !in_bounds(b < a.n_blocks, a.err)) return -1;
     return b;
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __gr
     }
     const int end = run_end;
     for (int r = row + tid; r < end; r += kAppendThreads)
-      if (block_at(r) == block) atomicMax(&owner[__ldg(a.slots + r) & (n_tok - 1)], r);
+      if (block_at(r) == block) atomicMax(&owner[a.slots[r] & (n_tok - 1)], r);
     __syncthreads();
     // amax over the rows that count
     float amax = 0.f;

@@ -1,127 +1,911 @@
 // Attention of a few query rows per request over the paged 8-bit context cache (include/dflash.h,
 // dflash_cache_attention):
-//   out_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale * q_i . k_j - max_j)
+//   out_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale * q_i . k_j)
 // over the cached keys that row i sees and, when given, the own rows of its request.
 //
-// One warp per (query row, query head): 32 keys at a time, one per lane, with an online softmax.
+// First kernel: 128 cached keys at a time on the fifth-generation tensor cores, straight from the
+// e4m3 codes as the copy engine brings them (no conversion in between):
+//   S[key][row]  = K Q^T   M = 128 keys,  N = query rows, K = head_dim   (kind::f8f6f4)
+//   O[d][row]   += V^T P   M = head_dim,  N = query rows, K = 128 keys
+// Keys are the tensor-memory lanes of S, so a thread owns a key: few rows fill every lane, a row's
+// softmax needs no exchange between threads while its reference stays (below), and a thread's
+// probabilities are contiguous bytes of the second product's operand. Queries and probabilities
+// are not e4m3 values, so both enter as sums of e4m3 terms side by side as further columns: a value's
+// nearest code, the nearest code of what that leaves, and so on. Two terms hold bf16's 8 significant
+// bits, three f16's 11. The terms' columns of S are added when it is read, those of O at the end.
+//
+//   t_ij = s_ij * q_scale_i * k_scale * scale * log2(e) + log2(v_scale)    (scales of the key's block)
+//   w_ij = 2^(t_ij - m_i)                       = p_ij * v_scale / 2^m_i
+//   O_i = sum_j w_ij * vcode_j,  L_i = sum_j w_ij / v_scale,  out_i = O_i / L_i
+// The reference m_i of a row is set so that its largest weight so far is 2^kTop, and moves only when a
+// weight would pass 2^kMax (kept below 448, the largest code): then L and O are rescaled. Weights of
+// 2^-4 and more keep all their bits; below, the subnormal codes' step of 2^-9 is the floor.
+//
+// Work is split by key tiles, not by requests: all tiles of all (request, KV head, row chunk) in one
+// line, an equal run of them for each CTA. A run may begin or end inside a (request, head, chunk); those
+// pieces are left as (O, m, L) for the second kernel, which joins them and attends over the own rows
+// in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "cache.h"
 #include "common.cuh"
+#include "tc05.cuh"
 
 namespace dfl {
 
 namespace {
 
-constexpr int kSimpleWarps = 4;
+constexpr int kTile = 128;               // keys per tile
+constexpr int kThreads = 192;            // warp 0: copies, warp 1: MMAs, warps 2-5: softmax
+constexpr int kMaxStages = 12;
+constexpr int kPBytes = kTile * 128;     // probabilities: 128 keys x up to 128 columns
+constexpr float kTop = 5.f, kMax = 8.75f;
+constexpr float kUnset = -1e30f;         // reference of a row that has seen no key
+constexpr int kRowArrays = 64;           // rows of the per-row arrays in shared memory
 
 __device__ __forceinline__ float row_f(__half v) { return __half2float(v); }
 __device__ __forceinline__ float row_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void row_store(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void row_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-__device__ __forceinline__ float code_f(uint8_t c) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half*>(&h));
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---- geometry ------------------------------------------------------------------------------------
+struct Request {
+  int req, row0, n;        // table row, first query row, query rows (0: nothing to do)
+  int len, lo;             // cached tokens; first position that any row sees
+  int s0, tiles;           // first position of tile 0 (a block boundary), key tiles
+  int chunks;
+};
+
+// First visible position of row i of the request, and one past its last (cached keys).
+__device__ __forceinline__ void row_range(const CacheAttnArgs& a, const Request& r, int i, int& lo, int& hi) {
+  const long long held = (long long)a.table_blocks << a.log_t;   // a ring holds the last ones
+  long long l = max(0LL, (long long)r.len - held), h = r.len;
+  if (a.causal) {
+    const long long at = a.k_own ? (long long)r.len + i : (long long)r.len - r.n + i;
+    h = min(h, at + 1);
+    if (a.window > 0) l = max(l, at + 1 - a.window);
+  } else if (a.window > 0) {
+    l = max(l, (long long)r.len - a.window);
+  }
+  lo = (int)l;
+  hi = (int)max(h, 0LL);
+}
+
+__device__ __forceinline__ Request request_of(const CacheAttnArgs& a, int b) {
+  Request r;
+  if (a.row_start) {
+    r.row0 = a.row_start[b];
+    r.n = min(a.row_start[b + 1] - r.row0, a.max_q);
+  } else {
+    r.row0 = b * a.max_q;
+    r.n = a.max_q;
+  }
+  r.req = a.requests ? a.requests[b] : b;
+  if (!in_bounds(r.n >= 0 && r.row0 >= 0 && r.row0 <= a.n_rows - r.n && r.req >= 0 && r.req < a.table_rows, a.err)) r.n = 0;
+  r.len = r.n > 0 ? min(max(a.lens[r.req], 0), 0x7fff0000) : 0;
+  int hi;
+  row_range(a, r, 0, r.lo, hi);
+  r.s0 = r.lo & ~((1 << a.log_t) - 1);
+  r.tiles = r.n > 0 && r.lo < r.len ? (r.len - r.s0 + kTile - 1) / kTile : 0;
+  r.chunks = (r.n * a.grp + a.p.rc - 1) / a.p.rc;
+  return r;
+}
+
+// A CTA's run of units (key tiles) is units [first, last) of all; CTA c of g gets an equal share.
+__device__ __forceinline__ long long unit_begin(int c, int total, int g) { return (long long)c * total / g; }
+
+// The tiles of one (request, KV head, row chunk) that a CTA's run holds.
+struct Segment {
+  Request r;
+  int b, pair, head, chunk;   // pair: over all requests, heads and chunks (with gaps)
+  int t0, t1;
+};
+
+struct Walk {
+  int u, u_end, b;
+  __device__ bool next(const CacheAttnArgs& a, const int* before, Segment& s) {
+    if (u >= u_end) return false;
+    while (u >= before[b + 1]) b++;
+    s.b = b;
+    s.r = request_of(a, b);
+    const int rem = u - before[b], p = rem / s.r.tiles;
+    s.head = p / s.r.chunks;
+    s.chunk = p % s.r.chunks;
+    s.pair = (b * a.n_kv + s.head) * a.p.chunks + s.chunk;
+    s.t0 = rem - p * s.r.tiles;
+    s.t1 = min(s.r.tiles, s.t0 + (u_end - u));
+    u += s.t1 - s.t0;
+    return true;
+  }
+};
+
+// ---- tensor-core pieces --------------------------------------------------------------------------
+// kind::f8f6f4, e4m3 x e4m3 -> fp32; the major bits (15, 16) say that an operand's rows run along
+// the contraction (MN-major).
+__device__ __forceinline__ constexpr uint32_t idesc_e4m3(int n, bool mn_major) {
+  return (1u << 4) | (mn_major ? (3u << 15) : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+
+// Shared-memory descriptor: swizzle 2 = 128 B, 4 = 64 B; sbo: bytes between groups of 8 rows (keys or
+// query rows), lbo: bytes between pieces of one swizzle width along an MN-major row.
+__device__ __forceinline__ constexpr uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)swizzle << 61);
+}
+
+__device__ __forceinline__ void umma_e4m3_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
+}
+
+// The sum of `TERMS` groups of 8 columns, `step` columns apart.
+template <int TERMS>
+__device__ __forceinline__ void tmem_sum8(uint32_t taddr, uint32_t step, float (&v)[8]) {
+  uint32_t r[8], s[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(s[0]),
+        "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]), "=r"(s[7])
+      : "r"(taddr), "r"(taddr + step)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]) + __uint_as_float(s[i]);
+  if constexpr (TERMS == 3) {
+    float w[8];
+    tmem_ld8(taddr + 2 * step, w);
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] += w[i];
+  }
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, int u, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(u), "r"(bar)
+      : "memory");
+}
+
+// Barrier of the four softmax warps; `any` returns whether any thread's predicate holds.
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+// 8 values per lane -> over the warp: lane l returns the reduction of value (l >> 2) & 7 (lanes of a
+// quad agree). Nine shuffles instead of forty.
+template <typename F>
+__device__ __forceinline__ float reduce8(const float (&v)[8], F f) {
+  const int lane = threadIdx.x & 31;
+  float a[4], b[2];
+  const bool hi = lane & 16;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const float mine = hi ? v[i + 4] : v[i], send = hi ? v[i] : v[i + 4];
+    a[i] = f(mine, __shfl_xor_sync(0xffffffffu, send, 16));
+  }
+  const bool hi2 = lane & 8;
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const float mine = hi2 ? a[i + 2] : a[i], send = hi2 ? a[i] : a[i + 2];
+    b[i] = f(mine, __shfl_xor_sync(0xffffffffu, send, 8));
+  }
+  const bool hi3 = lane & 4;
+  const float mine = hi3 ? b[1] : b[0], send = hi3 ? b[0] : b[1];
+  float c = f(mine, __shfl_xor_sync(0xffffffffu, send, 4));
+  c = f(c, __shfl_xor_sync(0xffffffffu, c, 2));
+  return f(c, __shfl_xor_sync(0xffffffffu, c, 1));
+}
+
+// 2^k >= 2^-64 with amax <= 448 * 2^k (amax finite): a row's largest value lands in (224, 448].
+__device__ __forceinline__ float row_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int k = (int)(u >> 23) - 135 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __int_as_float((max(k, kMinScaleExp) + 127) << 23);
+}
+
+// Two values as TERMS pairs of e4m3 codes (low byte: x), in f16: |x|, |y| <= 448. The first rounding, to
+// f16, is at the last term's level (2^-12).
+template <int TERMS>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&c)[TERMS]) {
+  __half2 v = __floats2half2_rn(x, y);
+#pragma unroll
+  for (int t = 0; t < TERMS; t++) {
+    const __half2_raw raw = *reinterpret_cast<const __half2_raw*>(&v);
+    const __nv_fp8x2_storage_t code = __nv_cvt_halfraw2_to_fp8x2(raw, __NV_SATFINITE, __NV_E4M3);
+    c[t] = code;
+    if (t + 1 < TERMS) {
+      const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(code, __NV_E4M3);
+      v = __hsub2(v, *reinterpret_cast<const __half2*>(&back));
+    }
+  }
+}
+
+// ---- shared memory -----------------------------------------------------------------------------------
+struct alignas(16) RowState {            // per query row of the CTA's chunk
+  float m[kRowArrays];                   // reference
+  float qs[kRowArrays];                  // the row's query scale
+  float f[kRowArrays];                   // factor of a moved reference; 1 / L at the end
+  float red[4][kRowArrays];              // per softmax warp: maxima, sums
+  int lo[kRowArrays], hi[kRowArrays];    // visible positions
+};
+
+__host__ __device__ constexpr int panels_of(int hd) { return hd == 256 ? 2 : 1; }
+__host__ __device__ constexpr int stage_bytes(int hd) { return kTile * hd; }
+
+__host__ __device__ inline size_t attn_fixed_smem(int hd, int n, int n_req) {
+  return (size_t)n * 128 * panels_of(hd) + kPBytes + sizeof(RowState) + (2 * kMaxStages + 8) * 8 + 36 + 4 * (size_t)(n_req + 1);
+}
+
+// ---- the first kernel ----------------------------------------------------------------------------------
+template <typename T, int HD, int RMAX>
+__global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
+    cache_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
+  constexpr int TERMS = sizeof(T) == 2 && __is_same(T, __nv_bfloat16) ? 2 : 3;
+  constexpr int PANELS = panels_of(HD), STAGE = stage_bytes(HD);
+  constexpr int ROWB = HD < 128 ? HD : 128;            // bytes of a key in a panel
+  constexpr int PANEL = kTile * 128;                   // bytes between panels (HD = 256)
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  const int S = a.p.stages, N = a.p.n, rp = a.p.rp;
+  uint8_t* ring = sm;
+  uint8_t* q_s = ring + (size_t)S * STAGE;
+  uint8_t* p_s = q_s + N * 128 * PANELS;
+  RowState& rs = *reinterpret_cast<RowState*>(p_s + kPBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(&rs + 1);
+  uint64_t *full = bars, *empty = bars + kMaxStages, *s_full = bars + 2 * kMaxStages, *s_free = s_full + 2, *q_full = s_full + 4,
+           *p_full = s_full + 5, *p_free = s_full + 6;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 8);
+  // Set when a wait gave up, in the entry of the current stretch between two points where all softmax threads
+  // look (just behind a barrier): entries alternate, so all of them see the same and leave together
+  volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* scan = reinterpret_cast<int*>(tmem_slot + 3);   // 6 warp sums
+  int* before = reinterpret_cast<int*>(tmem_slot + 9);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; i++) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&s_free[i]), 4);
+    }
+    mbar_init(smem_u32(q_full), 4);
+    mbar_init(smem_u32(p_full), 4);
+    mbar_init(smem_u32(p_free), 1);
+    mbar_init(smem_u32(s_full + 7), 1);
+    dead[0] = dead[1] = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), (uint32_t)a.p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc05_fence_before();
+  __syncthreads();
+  tc05_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Later kernels may start only now that this CTA holds its tensor memory: one that took it first would wait for
+  // this kernel, which would wait for it.
+  pdl_launch_dependents();
+  pdl_wait();
+  // key tiles before each request: one prefix sum over the requests, a few of them per thread
+  {
+    const int per = (a.n_req + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
+    int mine = 0;
+    for (int j = 0; j < per; j++)
+      if (b0 + j < a.n_req) {
+        const Request r = request_of(a, b0 + j);
+        const int u = r.tiles * r.chunks * a.n_kv;
+        before[b0 + j] = u;
+        mine += u;
+      }
+    int s = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += v;
+    }
+    if (lane == 31) scan[warp] = s;
+    __syncthreads();
+    int at = s - mine;
+    for (int w = 0; w < warp; w++) at += scan[w];
+    for (int j = 0; j < per; j++)
+      if (b0 + j < a.n_req) {
+        const int u = before[b0 + j];
+        before[b0 + j] = at;
+        at += u;
+        if (b0 + j == a.n_req - 1) before[a.n_req] = at;
+      }
+  }
+  __syncthreads();
+  const int total = before[a.n_req], ctas = min(a.grid, total);
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b <= a.n_req; b += kThreads) a.units[b] = before[b];
+  Walk walk{0, 0, 0};
+  if ((int)blockIdx.x < ctas) {
+    walk.u = (int)unit_begin(blockIdx.x, total, ctas);
+    walk.u_end = (int)unit_begin(blockIdx.x + 1, total, ctas);
+    int lo = 0, hi = a.n_req;                          // the request that holds the first unit
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= walk.u) lo = mid;
+      else hi = mid;
+    }
+    walk.b = lo;
+  }
+  // Ring order: K of a tile one step ahead of V of the one before: K0 K1 V0 K2 V1 .. V(n-1) per segment.
+  const uint32_t tmem_o = tmem + 2 * N;
+  Segment sg;
+
+  if (warp == 0) {
+    // ---- copies: one per block of the tile (and 128-byte panel), each by a lane of its own -------------
+    int seq = 0;
+    bool ok = true;
+    const int nb = kTile >> a.log_t;
+    while (ok && walk.next(a, before, sg)) {
+      auto entry_of = [&](int t) {                     // this lane's block of tile t, -1: nothing to copy
+        const int idx = (sg.r.s0 >> a.log_t) + t * nb + lane;
+        if (lane >= nb || t >= sg.t1 || ((long long)idx << a.log_t) >= sg.r.len) return -1;
+        const int e = *(a.table + (int64_t)sg.r.req * a.table_blocks + idx % a.table_blocks);
+        return in_bounds(e >= 0 && e < a.n_blocks, a.err) ? e : -1;
+      };
+      auto copy = [&](const CUtensorMap* map, int e) {
+        const int slot = seq % S;
+        if (seq >= S) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&empty[slot]), (seq / S + 1) & 1, a.err, kErrTimeoutCache));
+        if (!ok) return;
+        const uint32_t bar = smem_u32(&full[slot]);
+        const int n = __popc(__ballot_sync(0xffffffffu, e >= 0));
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * ((uint32_t)HD << a.log_t));
+        __syncwarp();
+        if (e >= 0) {
+          const uint32_t dst = smem_u32(ring + (size_t)slot * STAGE) + ((uint32_t)(lane * ROWB) << a.log_t);
+#pragma unroll
+          for (int p = 0; p < PANELS; p++) tma_load_5d(dst + p * PANEL, map, p * 128, 0, sg.head, e, a.layer, bar);
+        }
+        __syncwarp();
+        seq++;
+      };
+      int cur = entry_of(sg.t0), nxt = entry_of(sg.t0 + 1);
+      copy(&kmap, cur);
+      for (int t = sg.t0; ok && t < sg.t1; t++) {
+        const int far = entry_of(t + 2);
+        if (t + 1 < sg.t1) copy(&kmap, nxt);
+        if (ok) copy(&vmap, cur);
+        cur = nxt;
+        nxt = far;
+      }
+    }
+    // no copy may be in flight when the CTA leaves: the last fill of every stage has landed
+    for (int j = max(0, seq - S); j < seq; j++) mbar_wait_bounded(smem_u32(&full[j % S]), (j / S) & 1, nullptr, 0);
+  } else if (warp == 1) {
+    // ---- MMAs ---------------------------------------------------------------------------------------------
+    const uint32_t id_s = idesc_e4m3(N, false), id_o = idesc_e4m3(N, true);
+    const uint32_t ring_a = smem_u32(ring);
+    const uint64_t qd = smem_desc(smem_u32(q_s), 16, 1024, 2), pd = smem_desc(smem_u32(p_s), 16, 1024, 2);
+    int base = 0, g = 0, n_seg = 0, pv_done = 0;       // g: tiles so far
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int parity) {
+      return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), (uint32_t)parity & 1, a.err, kErrTimeoutCache));
+    };
+    while (ok && walk.next(a, before, sg)) {
+      const int n = sg.t1 - sg.t0;
+      ok = wait(q_full, n_seg);
+      n_seg++;
+      auto scores = [&](int t) {                       // tile t of the segment
+        const int sq = base + (t == 0 ? 0 : 2 * t - 1), slot = sq % S, gg = g + t;
+        ok = ok && wait(&full[slot], sq / S);
+        if (ok && gg >= 2) ok = wait(&s_free[gg & 1], (gg >> 1) + 1);
+        if (!ok) return;
+        tc05_fence_after();
+        const uint64_t kd = HD == 64 ? smem_desc(ring_a + slot * STAGE, 16, 512, 4) : smem_desc(ring_a + slot * STAGE, 16, 1024, 2);
+        const uint32_t d = tmem + (uint32_t)((gg & 1) * N);
+#pragma unroll
+        for (int ks = 0; ks < HD / 32; ks++) {
+          const uint64_t ka = kd + (uint64_t)((ks / 4) * (PANEL >> 4) + (ks % 4) * 2);
+          const uint64_t qa = qd + (uint64_t)((ks / 4) * (N * 8) + (ks % 4) * 2);
+          umma_e4m3_warp(d, ka, qa, id_s, ks > 0);
+        }
+        umma_commit_warp(smem_u32(&empty[slot]));
+        umma_commit_warp(smem_u32(&s_full[gg & 1]));
+      };
+      if (ok) scores(0);
+      for (int t = 0; ok && t < n; t++) {
+        if (t + 1 < n) scores(t + 1);
+        const int sq = base + (t + 1 < n ? 2 * t + 2 : 2 * n - 1), slot = sq % S, gg = g + t;
+        ok = ok && wait(&full[slot], sq / S) && wait(p_full, gg);
+        if (!ok) break;
+        tc05_fence_after();
+        const uint32_t va = ring_a + slot * STAGE;
+        const uint64_t vd = HD == 64 ? smem_desc(va, STAGE, 512, 4) : smem_desc(va, 16, 1024, 2);
+#pragma unroll
+        for (int p = 0; p < PANELS; p++)
+#pragma unroll
+          for (int ks = 0; ks < 4; ks++)
+            umma_e4m3_warp(tmem_o + p * N, vd + (uint64_t)((p * PANEL + ks * 32 * ROWB) >> 4), pd + (uint64_t)((ks * 32 * 128) >> 4),
+                           id_o, t > 0 || ks > 0);
+        umma_commit_warp(smem_u32(&empty[slot]));
+        umma_commit_warp(smem_u32(p_free));
+        pv_done = gg + 1;
+      }
+      base += 2 * n;
+      g += n;
+    }
+    // nothing of this CTA may still run on the tensor core when its memory is freed. After a wait that gave up
+    // there may be scores without a probability product: their commits have a barrier of their own
+    if (pv_done > 0) mbar_wait_bounded(smem_u32(p_free), (uint32_t)(pv_done - 1) & 1, a.err, kErrTimeoutCache);
+    if (!ok) {
+      umma_commit_warp(smem_u32(s_full + 7));
+      mbar_wait_bounded(smem_u32(s_full + 7), 0, nullptr, 0);
+    }
+  } else {
+    // ---- softmax ------------------------------------------------------------------------------------------
+    const int quarter = warp & 3, key = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t p_row = smem_u32(p_s) + key * 128;
+    int base = 0, g = 0, look = 0;
+    bool gone = false;
+    while (!gone && walk.next(a, before, sg)) {
+      const int n_tiles = sg.t1 - sg.t0, r0 = sg.chunk * a.p.rc, rows = min(a.p.rc, sg.r.n * a.grp - r0);
+      // rows of the chunk: visible range, query as e4m3 terms
+      if (key < rp) {
+        rs.m[key] = kUnset;
+        int lo = 0, hi = 0;
+        if (key < rows) row_range(a, sg.r, (r0 + key) / a.grp, lo, hi);
+        rs.lo[key] = lo;
+        rs.hi[key] = hi;
+      }
+      {
+        constexpr int kPerRow = HD / 8, kRowsAtOnce = 128 / kPerRow, kPasses = (RMAX + kRowsAtOnce - 1) / kRowsAtOnce;
+        const int c8 = (key % kPerRow) * 8;
+        uint4 v[kPasses];
+#pragma unroll
+        for (int u = 0; u < kPasses; u++) {
+          const int r = key / kPerRow + u * kRowsAtOnce;
+          v[u] = make_uint4(0, 0, 0, 0);
+          if (r < rows) {
+            const int row = sg.r.row0 + (r0 + r) / a.grp, head = sg.head * a.grp + (r0 + r) % a.grp;
+            v[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + row * a.q_row + head * a.q_head + c8);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kPasses; u++) {
+          const int r = key / kPerRow + u * kRowsAtOnce;
+          const T* e = reinterpret_cast<const T*>(&v[u]);
+          float x[8], amax = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            x[j] = row_f(e[j]);
+            const float m = fabsf(x[j]);
+            if (m <= 3.402823466e38f) amax = fmaxf(amax, m);
+            else x[j] = __int_as_float(0x7fffffff);    // an infinite query has no softmax
+          }
+#pragma unroll
+          for (int o = kPerRow / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const float sc = row_scale(amax), inv = 1.f / sc;
+          if (r < rp) {
+            uint32_t c[4][TERMS];
+#pragma unroll
+            for (int j = 0; j < 4; j++) split2<TERMS>(x[2 * j] * inv, x[2 * j + 1] * inv, c[j]);
+#pragma unroll
+            for (int t = 0; t < TERMS; t++) {
+              const int n = t * rp + r;
+              uint8_t* to = q_s + (c8 >> 7) * (N * 128) + n * 128 + ((((c8 & 127) >> 4) ^ (n & 7)) << 4) + (c8 & 8);
+              *reinterpret_cast<uint2*>(to) = make_uint2(c[0][t] | (c[1][t] << 16), c[2][t] | (c[3][t] << 16));
+            }
+            if (c8 == 0) rs.qs[r] = sc;
+          }
+        }
+      }
+      fence_proxy_async();
+      softmax_sync();
+      if (lane == 0) mbar_arrive(smem_u32(q_full));
+
+      int lo_all, hi_all, dummy;                       // keys that every row sees
+      row_range(a, sg.r, r0 / a.grp, dummy, hi_all);
+      row_range(a, sg.r, (r0 + rows - 1) / a.grp, lo_all, dummy);
+      // this thread's key of tile t: block number, then its scales (one and two tiles ahead)
+      auto block_of = [&](int t) {
+        const long long pos = (long long)sg.r.s0 + (long long)t * kTile + key;
+        if (t >= sg.t1 || pos >= sg.r.len) return -1;
+        const int e = *(a.table + (int64_t)sg.r.req * a.table_blocks + (int)(pos >> a.log_t) % a.table_blocks);
+        return e >= 0 && e < a.n_blocks ? e : -1;
+      };
+      int blk = block_of(sg.t0), blk_next = block_of(sg.t0 + 1);
+      auto scales = [&](int e, float& ks, float& vs) {
+        ks = 0.f, vs = 1.f;
+        if (e >= 0) {
+          ks = *(a.k_scale + (int64_t)e * a.n_kv + sg.head);
+          vs = *(a.v_scale + (int64_t)e * a.n_kv + sg.head);
+        }
+      };
+      float ks, vs;
+      scales(blk, ks, vs);
+      float l[RMAX];
+#pragma unroll
+      for (int r = 0; r < RMAX; r++) l[r] = 0.f;
+
+      for (int t = 0; t < n_tiles; t++) {
+        const int gg = g + t;
+        const int blk_far = block_of(sg.t0 + t + 2);
+        float ks_next, vs_next;
+        scales(blk_next, ks_next, vs_next);
+        const int pos = sg.r.s0 + (sg.t0 + t) * kTile + key;
+        const float ka = ks * a.scale_log2, v_floor = fmaxf(vs, __int_as_float((kMinScaleExp + 127) << 23));
+        const float vb = log2f(v_floor), v_inv = 1.f / v_floor;
+        const bool whole = blk >= 0 && pos >= lo_all && pos < hi_all;
+        if (!mbar_wait_bounded(smem_u32(&s_full[gg & 1]), (gg >> 1) & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
+        __syncwarp();
+        tc05_fence_after();
+        float tv[RMAX];
+        bool past = false;
+        const uint32_t ts = tmem + lanes + (uint32_t)((gg & 1) * N);
+#pragma unroll
+        for (int ch = 0; ch < RMAX / 8; ch++) {
+          if (ch * 8 < rp) {
+            float s8[8];
+            tmem_sum8<TERMS>(ts + ch * 8, rp, s8);
+#pragma unroll
+            for (int j = 0; j < 8; j++) tv[ch * 8 + j] = fmaf(s8[j] * rs.qs[ch * 8 + j], ka, vb);
+            if (!whole) {
+#pragma unroll
+              for (int j = 0; j < 8; j++)
+                if (!(blk >= 0 && pos >= rs.lo[ch * 8 + j] && pos < rs.hi[ch * 8 + j])) tv[ch * 8 + j] = -INFINITY;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j++) past |= tv[ch * 8 + j] - rs.m[ch * 8 + j] > kMax;
+          }
+        }
+        tc05_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s_free[gg & 1]));
+        const bool move = softmax_any(past);
+        gone = dead[look++ & 1];
+        if (gone) break;
+        if (move) {
+          // new references: a row's largest t over the tile at 2^kTop, where it passed 2^kMax
+#pragma unroll
+          for (int ch = 0; ch < RMAX / 8; ch++) {
+            if (ch * 8 < rp) {
+              float v8[8];
+#pragma unroll
+              for (int j = 0; j < 8; j++) v8[j] = tv[ch * 8 + j];
+              const float mx = reduce8(v8, [](float x, float y) { return fmaxf(x, y); });
+              if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = mx;
+            }
+          }
+          softmax_sync();
+          if (key < rp) {
+            const float mx = fmaxf(fmaxf(rs.red[0][key], rs.red[1][key]), fmaxf(rs.red[2][key], rs.red[3][key]));
+            const float old = rs.m[key], m = mx - old > kMax ? mx - kTop : old;
+            rs.m[key] = m;
+            rs.f[key] = m == old ? 1.f : ex2(old - m);
+          }
+          softmax_sync();
+#pragma unroll
+          for (int r = 0; r < RMAX; r++)
+            if (r < rp) l[r] *= rs.f[r];
+          if (t > 0) {
+            if (!mbar_wait_bounded(smem_u32(p_free), (gg - 1) & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
+            __syncwarp();
+            tc05_fence_after();
+            for (int col = 0; col < PANELS * TERMS; col++) {
+              const uint32_t to = tmem_o + lanes + (uint32_t)((col / TERMS) * N + (col % TERMS) * rp);
+              for (int ch = 0; ch < rp; ch += 8) {
+                float o8[8];
+                tmem_ld8(to + ch, o8);
+#pragma unroll
+                for (int j = 0; j < 8; j++) o8[j] *= rs.f[ch + j];
+                tmem_st8(to + ch, o8);
+              }
+            }
+            tmem_wait_st();
+          }
+        }
+        // the probabilities of the tile before have been read
+        if (gg > 0 && !mbar_wait_bounded(smem_u32(p_free), (gg - 1) & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
+        __syncwarp();
+        bool v_nan = false;
+        if (!whole) {
+          // A key that no row sees must not reach the product: its code bytes may be anything, and 0 * NaN
+          // is NaN. Nor may a NaN value reach the rows that do not see its key: there it becomes 0 and the
+          // weight becomes NaN for the rows that do.
+          const bool seen = blk >= 0 && pos >= sg.r.lo && pos < sg.r.len;
+          const int sq = base + (t + 1 < n_tiles ? 2 * t + 2 : 2 * n_tiles - 1), slot = sq % S;
+          if (!mbar_wait_bounded(smem_u32(&full[slot]), (sq / S) & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
+#pragma unroll
+          for (int p = 0; p < PANELS; p++)
+#pragma unroll
+            for (int c = 0; c < ROWB / 16; c++) {
+              uint4* at = reinterpret_cast<uint4*>(ring + (size_t)slot * STAGE + p * PANEL + key * ROWB + c * 16);
+              uint4 x = make_uint4(0, 0, 0, 0);
+              if (seen) {
+                x = *at;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                  const uint32_t bad = __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                  v_nan |= bad != 0;
+                  w[i] &= ~bad;
+                }
+              }
+              if (!seen || v_nan) *at = x;
+            }
+        }
+#pragma unroll
+        for (int ch = 0; ch < RMAX / 8; ch++) {
+          if (ch * 8 < rp) {
+            uint32_t c[4][TERMS];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+              float w0 = ex2(tv[ch * 8 + j] - rs.m[ch * 8 + j]), w1 = ex2(tv[ch * 8 + j + 1] - rs.m[ch * 8 + j + 1]);
+              if (v_nan) {
+                if (tv[ch * 8 + j] != -INFINITY) w0 = __int_as_float(0x7fffffff);
+                if (tv[ch * 8 + j + 1] != -INFINITY) w1 = __int_as_float(0x7fffffff);
+              }
+              l[ch * 8 + j] = fmaf(w0, v_inv, l[ch * 8 + j]);
+              l[ch * 8 + j + 1] = fmaf(w1, v_inv, l[ch * 8 + j + 1]);
+              split2<TERMS>(w0, w1, c[j / 2]);
+            }
+#pragma unroll
+            for (int i = 0; i < TERMS; i++) {
+              const int o = i * rp + ch * 8;
+              const uint32_t to = p_row + ((((uint32_t)o >> 4) ^ (key & 7)) << 4) + (o & 8);
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(c[0][i] | (c[1][i] << 16)),
+                           "r"(c[2][i] | (c[3][i] << 16))
+                           : "memory");
+            }
+          }
+        }
+        fence_proxy_async();
+        tc05_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(p_full));
+        blk = blk_next;
+        blk_next = blk_far;
+        ks = ks_next;
+        vs = vs_next;
+      }
+      base += 2 * n_tiles;
+      g += n_tiles;
+      if (gone) break;
+
+      // ---- end of the segment: L over the keys, then O -------------------------------------------------------
+#pragma unroll
+      for (int ch = 0; ch < RMAX / 8; ch++) {
+        if (ch * 8 < rp) {
+          float v8[8];
+#pragma unroll
+          for (int j = 0; j < 8; j++) v8[j] = l[ch * 8 + j];
+          const float sum = reduce8(v8, [](float x, float y) { return x + y; });
+          if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = sum;
+        }
+      }
+      if (!mbar_wait_bounded(smem_u32(p_free), (g - 1) & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
+      __syncwarp();
+      softmax_sync();
+      gone = dead[look++ & 1];
+      if (gone) break;
+      const bool direct = sg.t0 == 0 && sg.t1 == sg.r.tiles && !a.k_own;
+      const size_t slot = (size_t)blockIdx.x + sg.pair;
+      if (key < rp) {
+        const float L = (rs.red[0][key] + rs.red[1][key]) + (rs.red[2][key] + rs.red[3][key]);
+        rs.f[key] = L == 0.f ? 0.f : 1.f / L;
+        if (!direct) a.part_ml[slot * rp + key] = make_float2(rs.m[key], L);
+      }
+      softmax_sync();
+      tc05_fence_after();
+#pragma unroll
+      for (int p = 0; p < PANELS; p++) {
+        const int d = p * 128 + key;
+        for (int ch = 0; ch < rows; ch += 8) {
+          float o8[8];
+          tmem_sum8<TERMS>(tmem_o + lanes + (uint32_t)(p * N + ch), rp, o8);
+          if (key < HD) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+              const int r = ch + j;
+              if (r >= rows) break;
+              if (direct) {
+                const int row = sg.r.row0 + (r0 + r) / a.grp, head = sg.head * a.grp + (r0 + r) % a.grp;
+                row_store(static_cast<T*>(a.out) + row * a.o_row + head * a.o_head + d, o8[j] * rs.f[r]);
+              } else {
+                a.part_o[(slot * rp + r) * HD + d] = o8[j];
+              }
+            }
+          }
+        }
+      }
+      tc05_fence_before();
+      softmax_sync();                                  // rs belongs to the next segment now
+    }
+  }
+
+  tc05_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc05_fence_after();
+    tmem_dealloc(tmem, (uint32_t)a.p.tmem_cols);
+  }
+}
+
+// ---- the second kernel: join the pieces of a row, own rows, output; one warp per (request, head, row) --------
+constexpr int kJoinWarps = 4;
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
+  constexpr int PER = HD / 32;                         // columns per lane
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const long long task = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int r = (int)(task % a.p.rc), pair = (int)(task / a.p.rc);
+  const int chunk = pair % a.p.chunks, head = pair / a.p.chunks % a.n_kv, b = pair / a.p.chunks / a.n_kv;
+  if (b >= a.n_req) return;
+  const Request rq = request_of(a, b);
+  const int rr = chunk * a.p.rc + r;
+  if (rr >= rq.n * a.grp) return;
+  const int i = rr / a.grp, qh = head * a.grp + rr % a.grp, row = rq.row0 + i;
+  const int total = a.units[a.n_req], ctas = min(a.grid, total);
+  int c0 = 0, c1 = -1;                                 // CTAs that hold tiles of this row
+  if (rq.tiles > 0) {
+    const long long s = a.units[b] + (long long)(head * rq.chunks + chunk) * rq.tiles, e = s + rq.tiles;
+    c0 = (int)(((s + 1) * ctas - 1) / total);
+    c1 = (int)((e * ctas - 1) / total);
+    if (c0 == c1 && !a.k_own) return;                  // written by the first kernel
+  }
+  float m = -INFINITY, L = 0.f, o[PER];
+#pragma unroll
+  for (int c = 0; c < PER; c++) o[c] = 0.f;
+  auto take = [&](float mx, float w, const float (&v)[PER]) {   // add w (sum) and v at reference mx
+    const float mn = fmaxf(m, mx);
+    const float so = m == mn ? 1.f : ex2(m - mn), sn = mx == mn ? 1.f : ex2(mx - mn);
+    L = fmaf(w, sn, L * so);
+#pragma unroll
+    for (int c = 0; c < PER; c++) o[c] = fmaf(v[c], sn, o[c] * so);
+    m = mn;
+  };
+  for (int c = c0; c <= c1; c++) {
+    const size_t at = ((size_t)c + pair) * a.p.rp + r;
+    const float2 ml = __ldcg(&a.part_ml[at]);
+    float v[PER];
+#pragma unroll
+    for (int j = 0; j < PER; j++) v[j] = __ldcg(a.part_o + at * HD + lane * PER + j);
+    if (ml.x != kUnset) take(ml.x, ml.y, v);
+  }
+  if (a.k_own) {
+    float q[PER];
+    const T* qp = static_cast<const T*>(a.q) + row * a.q_row + qh * a.q_head + lane * PER;
+#pragma unroll
+    for (int j = 0; j < PER; j++) q[j] = row_f(qp[j]) * a.scale_log2;
+    const int j1 = a.causal ? i + 1 : rq.n, j0 = a.causal && a.window > 0 ? max(0, i + 1 - a.window) : 0;
+    for (int j = j0; j < j1; j++) {
+      const T* kp = static_cast<const T*>(a.k_own) + (rq.row0 + j) * a.ko_row + head * a.ko_head + lane * PER;
+      const T* vp = static_cast<const T*>(a.v_own) + (rq.row0 + j) * a.vo_row + head * a.vo_head + lane * PER;
+      float s = 0.f, v[PER];
+#pragma unroll
+      for (int c = 0; c < PER; c++) {
+        s = fmaf(q[c], row_f(kp[c]), s);
+        v[c] = row_f(vp[c]);
+      }
+      take(warp_sum(s), 1.f, v);
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  T* out = static_cast<T*>(a.out) + row * a.o_row + qh * a.o_head + lane * PER;
+#pragma unroll
+  for (int c = 0; c < PER; c++) row_store(out + c, o[c] * inv);
+}
+
+template <typename T, int HD, int RMAX>
+cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
+  static std::atomic<int> smem_set[kMaxDevices];
+  cudaError_t e = ensure_smem_limit(cache_attn_kernel<T, HD, RMAX>, a.p.smem, smem_set);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(cache_attn_kernel<T, HD, RMAX>, dim3(a.grid), dim3(kThreads), a.p.smem, s, a, kmap, vmap);
+  if (e != cudaSuccess) return e;
+  const long long tasks = (long long)a.n_req * a.n_kv * a.p.chunks * a.p.rc;
+  return launch_pdl(cache_attn_join_kernel<T, HD>, dim3((unsigned)((tasks + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, s, a);
 }
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kSimpleWarps * 32) cache_attn_simple_kernel(const __grid_constant__ CacheAttnArgs a) {
-  __shared__ float qs[kSimpleWarps][HD];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.z, i = blockIdx.y, head = blockIdx.x * kSimpleWarps + warp;
-  pdl_launch_dependents();
-  pdl_wait();
-  int row0, n;
-  if (a.row_start) {
-    row0 = a.row_start[b];
-    n = min(a.row_start[b + 1] - row0, a.max_q);
-  } else {
-    row0 = b * a.max_q;
-    n = a.max_q;
-  }
-  const int req = a.requests ? a.requests[b] : b;
-  if (i >= n || row0 < 0 || row0 + n > a.n_rows || head >= a.n_kv * a.grp || req < 0 || req >= a.table_rows) return;
-  const int kvh = head / a.grp, len = max(a.lens[req], 0), n_tok = 1 << a.log_t;
-  const bool own = a.k_own != nullptr;
-  const long long at = own ? (long long)len + i : (long long)len - n + i;
-  long long lo = 0, hi = len;
-  if (a.causal) {
-    if (at + 1 < hi) hi = at + 1 < 0 ? 0 : at + 1;
-    if (a.window > 0 && at + 1 - a.window > lo) lo = at + 1 - a.window;
-  } else if (a.window > 0 && (long long)len - a.window > lo) {
-    lo = (long long)len - a.window;
-  }
-  const T* q = static_cast<const T*>(a.q) + (int64_t)(row0 + i) * a.q_row + (int64_t)head * a.q_head;
-  for (int c = lane; c < HD; c += 32) qs[warp][c] = row_f(q[c]) * a.scale_log2;
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[HD / 32] = {};
-  const long long n_own = own ? n : 0;
-  for (long long j0 = lo; j0 < hi + n_own; j0 += 32) {
-    const long long j = j0 + lane;
-    float s = -INFINITY, vs = 0.f;
-    const uint8_t* vc = nullptr;
-    const T* vr = nullptr;
-    if (j < hi) {
-      const int blk = a.table[(int64_t)req * a.table_blocks + (j >> a.log_t) % a.table_blocks];
-      if (in_bounds(blk >= 0 && blk < a.n_blocks, a.err)) {
-        const int64_t off = blk * a.c_block + kvh * a.c_head + (j & (n_tok - 1)) * a.c_token;
-        vc = a.v + off;
-        vs = a.v_scale[(int64_t)blk * a.n_kv + kvh];
-        s = 0.f;
-        for (int c = 0; c < HD; c++) s = fmaf(qs[warp][c], code_f(a.k[off + c]), s);
-        s *= a.k_scale[(int64_t)blk * a.n_kv + kvh];
-      }
-    } else if (j < hi + n_own) {
-      const int jo = (int)(j - hi);
-      if (!a.causal || (jo <= i && (a.window <= 0 || jo > i - a.window))) {
-        const T* kr = static_cast<const T*>(a.k_own) + (int64_t)(row0 + jo) * a.ko_row + (int64_t)kvh * a.ko_head;
-        vr = static_cast<const T*>(a.v_own) + (int64_t)(row0 + jo) * a.vo_row + (int64_t)kvh * a.vo_head;
-        s = 0.f;
-        for (int c = 0; c < HD; c++) s = fmaf(qs[warp][c], row_f(kr[c]), s);
-      }
-    }
-    float cm = s;
-    for (int x = 16; x > 0; x >>= 1) cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, x));
-    const float mn = fmaxf(m, cm);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float alpha = exp2f(m - base);
-    const float p = vc || vr ? exp2f(s - base) : 0.f;
-    l = l * alpha + warp_sum(p);
-    m = mn;
-    for (int c = 0; c < HD / 32; c++) o[c] *= alpha;
-    for (int src = 0; src < 32; src++) {
-      const float ps = __shfl_sync(0xffffffffu, p, src), sc = __shfl_sync(0xffffffffu, vs, src);
-      const uint8_t* c8 = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vc), src));
-      const T* cr = reinterpret_cast<const T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vr), src));
-      if (c8)
-        for (int c = 0; c < HD / 32; c++) o[c] = fmaf(ps, code_f(c8[c * 32 + lane]) * sc, o[c]);
-      else if (cr)
-        for (int c = 0; c < HD / 32; c++) o[c] = fmaf(ps, row_f(cr[c * 32 + lane]), o[c]);
-    }
-  }
-  T* out = static_cast<T*>(a.out) + (int64_t)(row0 + i) * a.o_row + (int64_t)head * a.o_head;
-  for (int c = 0; c < HD / 32; c++) row_store(out + c * 32 + lane, l == 0.f ? 0.f : o[c] / l);
+cudaError_t launch_rows(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
+  if (a.p.rp <= 8) return launch<T, HD, 8>(a, kmap, vmap, s);
+  if (a.p.rp <= 40) return launch<T, HD, 40>(a, kmap, vmap, s);
+  if constexpr (__is_same(T, __nv_bfloat16)) return launch<T, HD, 64>(a, kmap, vmap, s);
+  return cudaErrorInvalidValue;
 }
 
 template <typename T>
-cudaError_t launch_simple(const CacheAttnArgs& a, cudaStream_t s) {
-  const dim3 grid((a.n_kv * a.grp + kSimpleWarps - 1) / kSimpleWarps, a.max_q, a.n_req), block(kSimpleWarps * 32);
+cudaError_t launch_hd(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
   switch (a.hd) {
-    case 64: return launch_pdl(cache_attn_simple_kernel<T, 64>, grid, block, 0, s, a);
-    case 128: return launch_pdl(cache_attn_simple_kernel<T, 128>, grid, block, 0, s, a);
-    case 256: return launch_pdl(cache_attn_simple_kernel<T, 256>, grid, block, 0, s, a);
+    case 64: return launch_rows<T, 64>(a, kmap, vmap, s);
+    case 128: return launch_rows<T, 128>(a, kmap, vmap, s);
+    case 256: return launch_rows<T, 256>(a, kmap, vmap, s);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_cache_attn(int dtype, const CacheAttnArgs& a, cudaStream_t s) {
-  return dtype == DFLASH_BF16 ? launch_simple<__nv_bfloat16>(a, s) : launch_simple<__half>(a, s);
+CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req) {
+  CacheAttnPlan p{};
+  p.terms = dtype == DFLASH_BF16 ? 2 : 3;
+  // at most 128 MMA columns: then two score buffers and the output fit tensor memory for every head_dim
+  const int limit = dtype == DFLASH_BF16 ? 64 : 40, rows = grp * max_q;
+  p.chunks = (rows + limit - 1) / limit;
+  p.rc = (rows + p.chunks - 1) / p.chunks;
+  p.rp = (p.rc + 7) / 8 * 8;
+  p.n = (p.terms * p.rp + 15) / 16 * 16;
+  const int cols = (2 + panels_of(hd)) * p.n;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < cols) p.tmem_cols *= 2;
+  const size_t fixed = attn_fixed_smem(hd, p.n, n_req) + 1024;
+  constexpr size_t kPerSm = 227 * 1024;
+  // two CTAs per SM where tensor memory allows it and each still holds four key or value tiles
+  const size_t half = kPerSm / 2 - 1024;
+  p.ctas_per_sm = p.tmem_cols <= 256 && fixed + 4 * (size_t)stage_bytes(hd) <= half ? 2 : 1;
+  const size_t room = (p.ctas_per_sm == 2 ? half : kPerSm) - fixed;
+  p.stages = (int)std::min<size_t>(kMaxStages, room / stage_bytes(hd));
+  p.smem = fixed + (size_t)p.stages * stage_bytes(hd);
+  return p;
+}
+
+cudaError_t launch_cache_attn(int dtype, const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                              cudaStream_t s) {
+  return dtype == DFLASH_BF16 ? launch_hd<__nv_bfloat16>(a, kmap, vmap, s) : launch_hd<__half>(a, kmap, vmap, s);
 }
 
 }  // namespace dfl

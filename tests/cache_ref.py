@@ -109,7 +109,7 @@ def attention(q, k_codes, v_codes, k_scale, v_scale, lens, table, counts, dtype,
         r = requests[b] if requests is not None else b
         length, width = lens[r], len(table[r])
         ids = [table[r][(p // T) % width] for p in range(length)]
-        there = torch.tensor([0 <= i < N for i in ids], dtype=torch.bool)
+        there = torch.tensor([0 <= i < N and p >= length - width * T for p, i in enumerate(ids)], dtype=torch.bool)
         safe = [i if 0 <= i < N else 0 for i in ids]
         at = [p % T for p in range(length)]
         k, v = kd[safe, :, at], vd[safe, :, at]                                     # [len][H][D]

@@ -284,6 +284,7 @@ def test_attention_ring_table_and_request_rows():
 
     run_attention(lens, [3] * 5, 4, 2, 128, T, "bf16", own=True, window=window, width=width, change=ring, seed=7)
     run_attention(lens, [2, 5, 1], 4, 2, 128, T, "bf16", causal=True, window=window, width=width, change=ring, requests=[4, 1, 3], seed=8)
+    run_attention(lens, [3] * 5, 4, 2, 128, T, "bf16", causal=True, width=width, change=ring, seed=9)     # no window: what the ring still holds
 
 
 def test_attention_garbage_in_masked_places():
