@@ -437,4 +437,9 @@ class Handle:
             pass
 
 
-from .cache import BlockPool, Cache  # noqa: E402,F401  (the binding of the paged context cache uses the names above)
+def __getattr__(name):
+    # the paged context cache's binding needs PyTorch at import; building the library does not
+    if name in ("BlockPool", "Cache"):
+        from . import cache
+        return getattr(cache, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -4,36 +4,52 @@ append and attention over the cache. Argument marshalling and checks only, as in
 from __future__ import annotations
 
 import ctypes
+import struct
 
-from . import (DFLASH_BF16, DFLASH_EINVAL, DFLASH_F16, DFLASH_F32, DFLASH_POOL_SCRATCH, DFlashError, _check, _stream_ptr,
+import torch
+
+from . import (DFLASH_BF16, DFLASH_EINVAL, DFLASH_F16, DFLASH_F32, DFLASH_POOL_MAX_REQUESTS, DFLASH_POOL_SCRATCH, DFlashError, _check,
                dflash_attention, dflash_cache_config, dflash_pool, dflash_rows, lib)
+
+_ROW_DTYPES = {torch.float32: DFLASH_F32, torch.bfloat16: DFLASH_BF16, torch.float16: DFLASH_F16}
+# dflash_attention, dflash_pool and dflash_rows as one struct.pack each: a call's arguments are a few dozen words, and
+# setting them one by one through ctypes takes longer than the kernels of a small call
+_ATTENTION, _POOL, _ROWS = struct.Struct("@6i4Qi4Q4Q4Q4Q2if"), struct.Struct("@5i5Q"), struct.Struct("@4Q")
+_NO_ROWS = (0, 0, 0, 0)
 
 
 def _row_dtype(t) -> int:
-    import torch
-    codes = {torch.float32: DFLASH_F32, torch.bfloat16: DFLASH_BF16, torch.float16: DFLASH_F16}
-    if t.dtype not in codes:
+    code = _ROW_DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"rows are fp32, bf16 or f16, not {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
 def _ints(name, t, n, device):
-    """The address of a contiguous int32 tensor of n elements (None: NULL)."""
-    import torch
+    """The address of a contiguous int32 tensor of n elements on CUDA device number `device` (None: NULL)."""
     if t is None:
-        return None
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.device != device or (n is not None and t.numel() != n):
-        raise ValueError(f"{name}: a contiguous int32 tensor{'' if n is None else f' of {n} elements'} on {device} is wanted")
+        return 0
+    if t.dtype is not torch.int32 or not t.is_contiguous() or t.get_device() != device or (n is not None and t.numel() != n):
+        raise ValueError(f"{name}: a contiguous int32 tensor{'' if n is None else f' of {n} elements'} on CUDA device {device} is wanted")
     return t.data_ptr()
 
 
-def _rows(name, t, shape, device, dtype):
-    """dflash_rows of a [..., rows, heads, head_dim] tensor with contiguous last dimension."""
+def _rows(name, t, n, heads, head_dim, device, dtype):
+    """The words of dflash_rows for a [..., n rows, heads, head_dim] tensor with contiguous last dimension."""
     if t is None:
-        return dflash_rows(None, 0, 0, 0)
-    if tuple(t.shape[-len(shape):]) != tuple(shape) or t.dim() > 4 or t.dtype != dtype or t.device != device or t.stride(-1) != 1:
-        raise ValueError(f"{name}: {dtype} rows of shape {tuple(shape)} on {device} are wanted, contiguous in the last dimension")
-    return dflash_rows(t.data_ptr(), t.stride(0) if t.dim() == 4 else 0, t.stride(-3), t.stride(-2))
+        return _NO_ROWS
+    shape, stride = t.shape, t.stride()
+    if not 3 <= len(shape) <= 4 or shape[-3] != n or shape[-2] != heads or shape[-1] != head_dim or t.dtype is not dtype \
+            or t.get_device() != device or stride[-1] != 1:
+        raise ValueError(f"{name}: {dtype} rows of shape {(n, heads, head_dim)} on CUDA device {device} are wanted, contiguous in the last dimension")
+    return t.data_ptr(), stride[0] if len(shape) == 4 else 0, stride[-3], stride[-2]
+
+
+def _raw_stream(stream, device):
+    """A cudaStream_t: the given stream's, or the one current on the tensors' device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 class BlockPool:
@@ -45,34 +61,36 @@ class BlockPool:
     """
 
     def __init__(self, block_tokens: int, max_requests: int | None = None, ring: bool = False, device="cuda"):
-        import torch
-        if block_tokens not in (16, 32, 64, 128) or (max_requests is not None and not 0 < max_requests <= 1024):
+        if block_tokens not in (16, 32, 64, 128) or (max_requests is not None and not 0 < max_requests <= DFLASH_POOL_MAX_REQUESTS):
             raise DFlashError(DFLASH_EINVAL, "BlockPool")
-        self.block_tokens, self.ring, self.max_requests = block_tokens, bool(ring), max_requests
+        self.block_tokens, self.ring, self.max_requests = block_tokens, int(ring), max_requests
         self.scratch = torch.zeros(DFLASH_POOL_SCRATCH, dtype=torch.uint8, device=device)
-        self.device = self.scratch.device
+        self.device = self.scratch.get_device()
+        self.p = dflash_pool()
+        self._reserve, self._truncate = lib().dflash_pool_reserve, lib().dflash_pool_truncate
 
-    def _pool(self, lens, table, free, free_count):
-        rows, blocks = table.shape
-        return dflash_pool(self.block_tokens, free.numel(), rows, blocks, int(self.ring), _ints("lens", lens, rows, self.device),
-                           _ints("table", table, None, self.device), _ints("free", free, None, self.device),
-                           _ints("free_count", free_count, 1, self.device), self.scratch.data_ptr())
+    def _pool(self, n, lens, table, free, free_count):
+        if self.max_requests is not None and n > self.max_requests:
+            raise DFlashError(DFLASH_EINVAL, f"BlockPool: {n} requests, limit {self.max_requests}")
+        (rows, blocks), d = table.shape, self.device
+        _POOL.pack_into(self.p, 0, self.block_tokens, free.numel(), rows, blocks, self.ring, _ints("lens", lens, rows, d),
+                        _ints("table", table, None, d), _ints("free", free, None, d), _ints("free_count", free_count, 1, d),
+                        self.scratch.data_ptr())
+        return ctypes.byref(self.p)
 
     def reserve(self, n_new, lens, table, free, free_count, slots, row_start, granted, requests=None, stream=None) -> int:
         """n_new[i] more tokens for table row requests[i] (None: row i); fills slots, row_start and granted."""
-        n = n_new.numel()
-        p = self._pool(lens, table, free, free_count)
-        d = self.device
-        return _check(lib().dflash_pool_reserve(ctypes.byref(p), n, _ints("requests", requests, n, d), _ints("n_new", n_new, n, d),
-                                                _ints("slots", slots, None, d), slots.numel(), _ints("row_start", row_start, n + 1, d),
-                                                _ints("granted", granted, n, d), _stream_ptr(stream)), "dflash_pool_reserve")
+        n, d = n_new.numel(), self.device
+        return _check(self._reserve(self._pool(n, lens, table, free, free_count), n, _ints("requests", requests, n, d),
+                                    _ints("n_new", n_new, n, d), _ints("slots", slots, None, d), slots.numel(),
+                                    _ints("row_start", row_start, n + 1, d), _ints("granted", granted, n, d),
+                                    _raw_stream(stream, d)), "dflash_pool_reserve")
 
     def truncate(self, new_len, lens, table, free, free_count, requests=None, stream=None) -> int:
         """Shorten table row requests[i] to new_len[i] tokens and give the blocks behind them back."""
-        n = new_len.numel()
-        p = self._pool(lens, table, free, free_count)
-        return _check(lib().dflash_pool_truncate(ctypes.byref(p), n, _ints("requests", requests, n, self.device),
-                                                 _ints("new_len", new_len, n, self.device), _stream_ptr(stream)), "dflash_pool_truncate")
+        n, d = new_len.numel(), self.device
+        return _check(self._truncate(self._pool(n, lens, table, free, free_count), n, _ints("requests", requests, n, d),
+                                     _ints("new_len", new_len, n, d), _raw_stream(stream, d)), "dflash_pool_truncate")
 
 
 class Cache:
@@ -85,7 +103,6 @@ class Cache:
     them the object appends only."""
 
     def __init__(self, k, v, k_scale, v_scale, max_requests: int = 0, max_q: int = 0, n_q_heads: int = 0, stream=None):
-        import torch
         layers, blocks, heads, tokens, head_dim = k.shape
         for name, t in (("k", k), ("v", v)):
             if t.dtype not in (torch.uint8, torch.float8_e4m3fn) or t.shape != k.shape or t.stride() != k.stride() or t.stride(-1) != 1 \
@@ -95,7 +112,7 @@ class Cache:
             if t.dtype != torch.float32 or tuple(t.shape) != (layers, blocks, heads) or not t.is_contiguous() or t.device != k.device:
                 raise ValueError(f"{name}: contiguous fp32 [layers][blocks][heads] is wanted")
         self.tensors = (k, v, k_scale, v_scale)
-        self.device, self.heads, self.head_dim = k.device, heads, head_dim
+        self.device, self.heads, self.head_dim = k.get_device(), heads, head_dim
         self.n_q_heads, self.max_q = n_q_heads, max_q
         cfg = dflash_cache_config(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), layers, blocks, tokens,
                                   heads, head_dim, *k.stride()[:4], n_q_heads, max_requests, max_q)
@@ -105,22 +122,23 @@ class Cache:
         self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=k.device)
         base = (self.workspace.data_ptr() + 255) // 256 * 256
         h = ctypes.c_void_p()
-        _check(lib().dflash_cache_create(ctypes.byref(cfg), base, nbytes, _stream_ptr(stream), ctypes.byref(h)), "dflash_cache_create")
+        _check(lib().dflash_cache_create(ctypes.byref(cfg), base, nbytes, _raw_stream(stream, self.device), ctypes.byref(h)),
+               "dflash_cache_create")
         self.h = h
+        self._k, self._v, self._a = dflash_rows(), dflash_rows(), dflash_attention()
+        self._append, self._attention = lib().dflash_cache_append, lib().dflash_cache_attention
 
     def append(self, slots, k_rows, v_rows, layer: int = 0, stream=None) -> int:
         """Quantise rows [layers'][n][KV heads][head_dim] (or [n][KV heads][head_dim]: one layer) into their
         slots, for layers layer .. layer + layers' - 1."""
-        n = slots.numel()
-        shape = (n, self.heads, self.head_dim)
-        dtype = _row_dtype(k_rows)
-        n_layers = k_rows.shape[0] if k_rows.dim() == 4 else 1
+        n, d, dt = slots.numel(), self.device, k_rows.dtype
         if v_rows.shape != k_rows.shape:
             raise ValueError("k_rows and v_rows have different shapes")
-        k = _rows("k_rows", k_rows, shape, self.device, k_rows.dtype)
-        v = _rows("v_rows", v_rows, shape, self.device, k_rows.dtype)
-        return _check(lib().dflash_cache_append(self.h, layer, n_layers, n, _ints("slots", slots, n, self.device), ctypes.byref(k),
-                                                ctypes.byref(v), dtype, _stream_ptr(stream)), "dflash_cache_append")
+        _ROWS.pack_into(self._k, 0, *_rows("k_rows", k_rows, n, self.heads, self.head_dim, d, dt))
+        _ROWS.pack_into(self._v, 0, *_rows("v_rows", v_rows, n, self.heads, self.head_dim, d, dt))
+        return _check(self._append(self.h, layer, k_rows.shape[0] if k_rows.dim() == 4 else 1, n, _ints("slots", slots, n, d),
+                                   ctypes.byref(self._k), ctypes.byref(self._v), _row_dtype(k_rows), _raw_stream(stream, d)),
+                      "dflash_cache_append")
 
     def attention(self, q, lens, table, out, layer: int = 0, row_start=None, max_q: int | None = None, k_own=None, v_own=None,
                   window: int = 0, causal: bool = False, scale: float | None = None, requests=None, stream=None) -> int:
@@ -130,8 +148,7 @@ class Cache:
         when row_start is given, else to rows / requests. scale defaults to head_dim ** -0.5."""
         if not self.max_q:
             raise DFlashError(DFLASH_EINVAL, "dflash_cache_attention (the cache was made without attention limits)")
-        d, dt, n_rows = self.device, q.dtype, q.shape[0]
-        dtype = _row_dtype(q)
+        d, dt, n_rows, heads, hd = self.device, q.dtype, q.shape[0], self.heads, self.head_dim
         table_rows, table_blocks = table.shape
         if requests is not None:
             n_req = requests.numel()
@@ -141,17 +158,15 @@ class Cache:
             n_req = lens.numel()
         if max_q is None:
             max_q = self.max_q if row_start is not None else n_rows // max(n_req, 1)
-        q_shape, kv_shape = (n_rows, self.n_q_heads, self.head_dim), (n_rows, self.heads, self.head_dim)
-        a = dflash_attention(layer, n_req, n_rows, max_q, table_rows, table_blocks, _ints("requests", requests, n_req, d),
+        _ATTENTION.pack_into(self._a, 0, layer, n_req, n_rows, max_q, table_rows, table_blocks, _ints("requests", requests, n_req, d),
                              _ints("lens", lens, table_rows, d), _ints("table", table, None, d),
-                             _ints("row_start", row_start, n_req + 1, d), dtype, _rows("q", q, q_shape, d, dt),
-                             _rows("out", out, q_shape, d, dt), _rows("k_own", k_own, kv_shape, d, dt),
-                             _rows("v_own", v_own, kv_shape, d, dt), int(causal), window,
-                             self.head_dim ** -0.5 if scale is None else scale)
-        return _check(lib().dflash_cache_attention(self.h, ctypes.byref(a), _stream_ptr(stream)), "dflash_cache_attention")
+                             _ints("row_start", row_start, n_req + 1, d), _row_dtype(q), *_rows("q", q, n_rows, self.n_q_heads, hd, d, dt),
+                             *_rows("out", out, n_rows, self.n_q_heads, hd, d, dt), *_rows("k_own", k_own, n_rows, heads, hd, d, dt),
+                             *_rows("v_own", v_own, n_rows, heads, hd, d, dt), causal, window, hd ** -0.5 if scale is None else scale)
+        return _check(self._attention(self.h, ctypes.byref(self._a), _raw_stream(stream, d)), "dflash_cache_attention")
 
     def check_errors(self, stream=None) -> int:
-        return _check(lib().dflash_cache_check_errors(self.h, _stream_ptr(stream)), "dflash_cache_check_errors")
+        return _check(lib().dflash_cache_check_errors(self.h, _raw_stream(stream, self.device)), "dflash_cache_check_errors")
 
     def close(self):
         if getattr(self, "h", None):

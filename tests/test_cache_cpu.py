@@ -31,6 +31,15 @@ def test_struct_layouts_match_c(tmp_path):
             ctypes.sizeof(pkg.dflash_attention), pkg.dflash_cache_config.max_q.offset, pkg.dflash_attention.k_own.offset,
             pkg.dflash_attention.scale.offset]
     assert got == want
+    # the binding packs three of them in one go
+    from speculative_block_draft_gb300 import cache
+    assert cache._ROWS.size == ctypes.sizeof(pkg.dflash_rows) and cache._POOL.size == ctypes.sizeof(pkg.dflash_pool)
+    assert cache._ATTENTION.size == pkg.dflash_attention.scale.offset + 4
+    a = pkg.dflash_attention()
+    cache._ATTENTION.pack_into(a, 0, *range(1, 12), *range(20, 36), 40, 41, 0.5)
+    assert (a.layer, a.table_blocks, a.requests, a.row_start, a.dtype, a.causal, a.window, a.scale) == (1, 6, 7, 10, 11, 40, 41, 0.5)
+    assert [(r.data, r.layer_stride, r.row_stride, r.head_stride) for r in (a.q, a.out, a.k_own, a.v_own)] == \
+        [tuple(range(i, i + 4)) for i in (20, 24, 28, 32)]
 
 
 def config(**kw):
