@@ -20,7 +20,7 @@ struct CacheAppendArgs {
   int64_t row_layer[2], row_row[2], row_head[2];   // strides of the rows, elements
   int64_t c_layer, c_block, c_head, c_token;       // strides of the codes, bytes
   int layer0, n_layers, n_rows, n_blocks, n_kv, hd, log_t;
-  int rows_per_cta;
+  int heads, rows_per_cta;  // set by the launcher
   const int32_t* slots;
   unsigned* err;
 };

@@ -193,7 +193,6 @@ int dflash_cache_append(dflash_cache* c, int layer, int n_layers, int n_rows, co
   a.n_kv = f.n_kv_heads;
   a.hd = f.head_dim;
   a.log_t = c->log_t;
-  a.rows_per_cta = n_rows <= 1024 ? 1 : 16;
   a.slots = slots;
   a.err = c->err;
   return status_of(launch_cache_append(dtype, a, static_cast<cudaStream_t>(stream)));
