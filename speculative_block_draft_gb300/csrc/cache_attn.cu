@@ -41,7 +41,9 @@ namespace dfl {
 namespace {
 
 constexpr int kTile = 128;               // keys per tile
-constexpr int kThreads = 192;            // warp 0: copies, warp 1: MMAs, warps 2-5: softmax
+// Warp 0: copies, warp 1: MMAs, then one or two groups of four softmax warps. The groups share a tile's keys and
+// split its query rows: each has its own rows' references, barrier and part of the output.
+__host__ __device__ constexpr int threads_of(int groups) { return 64 + 128 * groups; }
 constexpr int kMaxStages = 12;
 constexpr int kPBytes = kTile * 128;     // probabilities: 128 keys x up to 128 columns
 constexpr float kTop = 5.f, kMax = 8.75f;
@@ -82,18 +84,26 @@ __device__ __forceinline__ void row_range(const CacheAttnArgs& a, const Request&
   hi = (int)max(h, 0LL);
 }
 
-__device__ __forceinline__ Request request_of(const CacheAttnArgs& a, int b) {
-  Request r;
+// What a call says about request b: first query row, query rows, cached tokens, table row.
+__device__ __forceinline__ int4 read_request(const CacheAttnArgs& a, int b) {
+  int row0 = b * a.max_q, n = a.max_q;
+  const int req = a.requests ? a.requests[b] : b;
   if (a.row_start) {
-    r.row0 = a.row_start[b];
-    r.n = min(a.row_start[b + 1] - r.row0, a.max_q);
-  } else {
-    r.row0 = b * a.max_q;
-    r.n = a.max_q;
+    row0 = a.row_start[b];
+    n = min(a.row_start[b + 1] - row0, a.max_q);
   }
-  r.req = a.requests ? a.requests[b] : b;
-  if (!in_bounds(r.n >= 0 && r.row0 >= 0 && r.row0 <= a.n_rows - r.n && r.req >= 0 && r.req < a.table_rows, a.err)) r.n = 0;
-  r.len = r.n > 0 ? min(max(a.lens[r.req], 0), 0x7fff0000) : 0;
+  const bool known = req >= 0 && req < a.table_rows;
+  const int len = a.lens[known ? req : 0];
+  if (!in_bounds(n >= 0 && row0 >= 0 && row0 <= a.n_rows - n && known, a.err)) n = 0;
+  return make_int4(row0, n, n > 0 ? min(max(len, 0), 0x7fff0000) : 0, req);
+}
+
+__device__ __forceinline__ Request request_of(const CacheAttnArgs& a, int4 w) {
+  Request r;
+  r.row0 = w.x;
+  r.n = w.y;
+  r.len = w.z;
+  r.req = w.w;
   int hi;
   row_range(a, r, 0, r.lo, hi);
   r.s0 = r.lo & ~((1 << a.log_t) - 1);
@@ -114,11 +124,11 @@ struct Segment {
 
 struct Walk {
   int u, u_end, b;
-  __device__ bool next(const CacheAttnArgs& a, const int* before, Segment& s) {
+  __device__ bool next(const CacheAttnArgs& a, const int* before, const int4* words, Segment& s) {
     if (u >= u_end) return false;
     while (u >= before[b + 1]) b++;
     s.b = b;
-    s.r = request_of(a, b);
+    s.r = request_of(a, words[b]);
     const int rem = u - before[b], p = rem / s.r.tiles;
     s.head = p / s.r.chunks;
     s.chunk = p % s.r.chunks;
@@ -206,19 +216,31 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Barrier of the four softmax warps; `any` returns whether any thread's predicate holds.
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_any(bool v) {
+// Barrier of the four warps of softmax group `id`; `any` returns whether any thread's predicate holds.
+__device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id + 1) : "memory"); }
+__device__ __forceinline__ bool group_any(int id, bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.aligned.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.aligned.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)v)
+      : "r"((uint32_t)v), "r"(id + 1)
       : "memory");
   return r != 0;
+}
+
+// log2 and reciprocal of a scale, exact for the powers of two that the append writes.
+__device__ __forceinline__ void scale_terms(float v, float& lg, float& inv) {
+  const uint32_t u = __float_as_uint(v);
+  if ((u & 0x7fffffu) == 0 && u < 0x7f000000u) {       // 2^-64 <= v <= 2^126
+    lg = (float)((int)(u >> 23) - 127);
+    inv = __uint_as_float((254u << 23) - u);
+  } else {
+    lg = log2f(v);
+    inv = 1.f / v;
+  }
 }
 
 // 8 values per lane -> over the warp: lane l returns the reduction of value (l >> 2) & 7 (lanes of a
@@ -273,24 +295,28 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&c)[TERMS]) {
 // ---- shared memory -----------------------------------------------------------------------------------
 struct alignas(16) RowState {            // per query row of the CTA's chunk
   float m[kRowArrays];                   // reference
+  float past[kRowArrays];                // reference + kMax: a larger t moves it
   float qs[kRowArrays];                  // the row's query scale
   float f[kRowArrays];                   // factor of a moved reference; 1 / L at the end
   float red[4][kRowArrays];              // per softmax warp: maxima, sums
   int lo[kRowArrays], hi[kRowArrays];    // visible positions
+  int nan_tile[kTile];                   // per key: 1 + the last tile whose value had a NaN that was cleared
 };
 
 __host__ __device__ constexpr int panels_of(int hd) { return hd == 256 ? 2 : 1; }
 __host__ __device__ constexpr int stage_bytes(int hd) { return kTile * hd; }
 
 __host__ __device__ inline size_t attn_fixed_smem(int hd, int n, int n_req) {
-  return (size_t)n * 128 * panels_of(hd) + kPBytes + sizeof(RowState) + (2 * kMaxStages + 8) * 8 + 36 + 4 * (size_t)(n_req + 1);
+  return (size_t)n * 128 * panels_of(hd) + kPBytes + sizeof(RowState) + (2 * kMaxStages + 8) * 8 + 64 + 20 * (size_t)(n_req + 1);
 }
 
 // ---- the first kernel ----------------------------------------------------------------------------------
-template <typename T, int HD, int RMAX>
-__global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
+// GROUPS softmax groups of at most 8 * GC rows each.
+template <typename T, int HD, int GROUPS, int GC>
+__global__ void __launch_bounds__(threads_of(GROUPS), GC <= 3 ? 2 : 1)
     cache_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
+  constexpr int kThreads = threads_of(GROUPS), kWarps = kThreads / 32;
   constexpr int TERMS = sizeof(T) == 2 && __is_same(T, __nv_bfloat16) ? 2 : 3;
   constexpr int PANELS = panels_of(HD), STAGE = stage_bytes(HD);
   constexpr int ROWB = HD < 128 ? HD : 128;            // bytes of a key in a panel
@@ -306,11 +332,12 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
   uint64_t *full = bars, *empty = bars + kMaxStages, *s_full = bars + 2 * kMaxStages, *s_free = s_full + 2, *q_full = s_full + 4,
            *p_full = s_full + 5, *p_free = s_full + 6;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 8);
-  // Set when a wait gave up, in the entry of the current stretch between two points where all softmax threads
-  // look (just behind a barrier): entries alternate, so all of them see the same and leave together
-  volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* scan = reinterpret_cast<int*>(tmem_slot + 3);   // 6 warp sums
-  int* before = reinterpret_cast<int*>(tmem_slot + 9);
+  // Set when a softmax wait gave up: per group, and by turns for the stretches between two points where all of its
+  // threads look (just behind a barrier), so that all of them see the same and leave together
+  volatile int* dead_flags = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* scan = reinterpret_cast<int*>(tmem_slot + 5);   // warp sums
+  int4* words = reinterpret_cast<int4*>(tmem_slot + 16);
+  int* before = reinterpret_cast<int*>(words + a.n_req);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -320,13 +347,14 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
     }
     for (int i = 0; i < 2; i++) {
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&s_free[i]), 4);
+      mbar_init(smem_u32(&s_free[i]), 4 * GROUPS);
     }
-    mbar_init(smem_u32(q_full), 4);
-    mbar_init(smem_u32(p_full), 4);
+    mbar_init(smem_u32(q_full), 4 * GROUPS);
+    mbar_init(smem_u32(p_full), 4 * GROUPS);
     mbar_init(smem_u32(p_free), 1);
     mbar_init(smem_u32(s_full + 7), 1);
-    dead[0] = dead[1] = 0;
+    for (int i = 0; i < 4; i++) dead_flags[i] = 0;
+    for (int i = 0; i < kTile; i++) rs.nan_tile[i] = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -347,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
     int mine = 0;
     for (int j = 0; j < per; j++)
       if (b0 + j < a.n_req) {
-        const Request r = request_of(a, b0 + j);
+        words[b0 + j] = read_request(a, b0 + j);
+        const Request r = request_of(a, words[b0 + j]);
         const int u = r.tiles * r.chunks * a.n_kv;
         before[b0 + j] = u;
         mine += u;
@@ -361,7 +390,8 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
     if (lane == 31) scan[warp] = s;
     __syncthreads();
     int at = s - mine;
-    for (int w = 0; w < warp; w++) at += scan[w];
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) at += w < warp ? scan[w] : 0;
     for (int j = 0; j < per; j++)
       if (b0 + j < a.n_req) {
         const int u = before[b0 + j];
@@ -395,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
     int seq = 0;
     bool ok = true;
     const int nb = kTile >> a.log_t;
-    while (ok && walk.next(a, before, sg)) {
+    while (ok && walk.next(a, before, words, sg)) {
       auto entry_of = [&](int t) {                     // this lane's block of tile t, -1: nothing to copy
         const int idx = (sg.r.s0 >> a.log_t) + t * nb + lane;
         if (lane >= nb || t >= sg.t1 || ((long long)idx << a.log_t) >= sg.r.len) return -1;
@@ -440,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
     auto wait = [&](uint64_t* bar, int parity) {
       return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), (uint32_t)parity & 1, a.err, kErrTimeoutCache));
     };
-    while (ok && walk.next(a, before, sg)) {
+    while (ok && walk.next(a, before, words, sg)) {
       const int n = sg.t1 - sg.t0;
       ok = wait(q_full, n_seg);
       n_seg++;
@@ -492,38 +522,50 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
     }
   } else {
     // ---- softmax ------------------------------------------------------------------------------------------
-    const int quarter = warp & 3, key = quarter * 32 + lane;
+    const int group = GROUPS == 1 ? 0 : (warp - 2) >> 2, quarter = warp & 3, key = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t p_row = smem_u32(p_s) + key * 128;
+    volatile int* dead = dead_flags + 2 * group;
+    const int half = (rp / 8 + GROUPS - 1) / GROUPS;                      // chunks of 8 rows: this group's first, and one past
+    const int ch0 = group * half, n_ch = min(half, rp / 8 - ch0), g0 = ch0 * 8;
     int base = 0, g = 0, look = 0;
     bool gone = false;
-    while (!gone && walk.next(a, before, sg)) {
+    auto wait = [&](uint64_t* bar, int parity) {
+      if (!mbar_wait_bounded(smem_u32(bar), (uint32_t)parity & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
+      __syncwarp();
+    };
+    while (!gone && walk.next(a, before, words, sg)) {
       const int n_tiles = sg.t1 - sg.t0, r0 = sg.chunk * a.p.rc, rows = min(a.p.rc, sg.r.n * a.grp - r0);
-      // rows of the chunk: visible range, query as e4m3 terms
-      if (key < rp) {
-        rs.m[key] = kUnset;
+      // the group's rows: visible range, query as e4m3 terms
+      if (key < n_ch * 8) {
+        const int r = g0 + key;
+        rs.m[r] = kUnset;
+        rs.past[r] = kUnset;
         int lo = 0, hi = 0;
-        if (key < rows) row_range(a, sg.r, (r0 + key) / a.grp, lo, hi);
-        rs.lo[key] = lo;
-        rs.hi[key] = hi;
+        if (r < rows) row_range(a, sg.r, (r0 + r) / a.grp, lo, hi);
+        rs.lo[r] = lo;
+        rs.hi[r] = hi;
       }
       {
-        constexpr int kPerRow = HD / 8, kRowsAtOnce = 128 / kPerRow, kPasses = (RMAX + kRowsAtOnce - 1) / kRowsAtOnce;
+        constexpr int kPerRow = HD / 8, kRowsAtOnce = 128 / kPerRow, kPasses = (GC * 8 + kRowsAtOnce - 1) / kRowsAtOnce;
         const int c8 = (key % kPerRow) * 8;
         uint4 v[kPasses];
 #pragma unroll
         for (int u = 0; u < kPasses; u++) {
-          const int r = key / kPerRow + u * kRowsAtOnce;
+          const int r = g0 + key / kPerRow + u * kRowsAtOnce;
           v[u] = make_uint4(0, 0, 0, 0);
-          if (r < rows) {
+          if (r < rows && r < g0 + n_ch * 8) {
             const int row = sg.r.row0 + (r0 + r) / a.grp, head = sg.head * a.grp + (r0 + r) % a.grp;
             v[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + row * a.q_row + head * a.q_head + c8);
           }
         }
-#pragma unroll
+#pragma unroll 1
         for (int u = 0; u < kPasses; u++) {
-          const int r = key / kPerRow + u * kRowsAtOnce;
-          const T* e = reinterpret_cast<const T*>(&v[u]);
+          const int r = g0 + key / kPerRow + u * kRowsAtOnce;
+          const uint4 now = v[0];                      // the passes move down: one copy of this code
+#pragma unroll
+          for (int w = 0; w + 1 < kPasses; w++) v[w] = v[w + 1];
+          const T* e = reinterpret_cast<const T*>(&now);
           float x[8], amax = 0.f;
 #pragma unroll
           for (int j = 0; j < 8; j++) {
@@ -534,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
           }
 #pragma unroll
           for (int o = kPerRow / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          const float sc = row_scale(amax), inv = 1.f / sc;
-          if (r < rp) {
+          const float sc = row_scale(amax), inv = __uint_as_float((254u << 23) - __float_as_uint(sc));
+          if (r < g0 + n_ch * 8) {
             uint32_t c[4][TERMS];
 #pragma unroll
             for (int j = 0; j < 4; j++) split2<TERMS>(x[2 * j] * inv, x[2 * j + 1] * inv, c[j]);
@@ -550,8 +592,9 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
         }
       }
       fence_proxy_async();
-      softmax_sync();
+      __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(q_full));
+      group_sync(group);
 
       int lo_all, hi_all, dummy;                       // keys that every row sees
       row_range(a, sg.r, r0 / a.grp, dummy, hi_all);
@@ -573,81 +616,98 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
       };
       float ks, vs;
       scales(blk, ks, vs);
-      float l[RMAX];
+      float l[GC * 8];
 #pragma unroll
-      for (int r = 0; r < RMAX; r++) l[r] = 0.f;
+      for (int r = 0; r < GC * 8; r++) l[r] = 0.f;
 
+#pragma unroll 1
       for (int t = 0; t < n_tiles; t++) {
         const int gg = g + t;
         const int blk_far = block_of(sg.t0 + t + 2);
         float ks_next, vs_next;
         scales(blk_next, ks_next, vs_next);
         const int pos = sg.r.s0 + (sg.t0 + t) * kTile + key;
-        const float ka = ks * a.scale_log2, v_floor = fmaxf(vs, __int_as_float((kMinScaleExp + 127) << 23));
-        const float vb = log2f(v_floor), v_inv = 1.f / v_floor;
-        const bool whole = blk >= 0 && pos >= lo_all && pos < hi_all;
-        if (!mbar_wait_bounded(smem_u32(&s_full[gg & 1]), (gg >> 1) & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
-        __syncwarp();
+        const float ka = ks * a.scale_log2;
+        float vb, v_inv;
+        scale_terms(fmaxf(vs, __int_as_float((kMinScaleExp + 127) << 23)), vb, v_inv);
+        const bool seen = blk >= 0 && pos >= sg.r.lo && pos < sg.r.len;      // by some row
+        const bool whole = seen && pos >= lo_all && pos < hi_all;            // by every row
+        wait(&s_full[gg & 1], gg >> 1);
         tc05_fence_after();
-        float tv[RMAX];
+        float tv[GC * 8];
         bool past = false;
-        const uint32_t ts = tmem + lanes + (uint32_t)((gg & 1) * N);
+        const uint32_t ts = tmem + lanes + (uint32_t)((gg & 1) * N + g0);
 #pragma unroll
-        for (int ch = 0; ch < RMAX / 8; ch++) {
-          if (ch * 8 < rp) {
+        for (int ch = 0; ch < GC; ch++) {
+          if (ch < n_ch) {
             float s8[8];
             tmem_sum8<TERMS>(ts + ch * 8, rp, s8);
+            const float4* qs = reinterpret_cast<const float4*>(&rs.qs[g0 + ch * 8]);
+            const float4* pt = reinterpret_cast<const float4*>(&rs.past[g0 + ch * 8]);
+            const float4 q0 = qs[0], q1 = qs[1], p0 = pt[0], p1 = pt[1];
+            const float q8[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+            const float p8[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
-            for (int j = 0; j < 8; j++) tv[ch * 8 + j] = fmaf(s8[j] * rs.qs[ch * 8 + j], ka, vb);
-            if (!whole) {
-#pragma unroll
-              for (int j = 0; j < 8; j++)
-                if (!(blk >= 0 && pos >= rs.lo[ch * 8 + j] && pos < rs.hi[ch * 8 + j])) tv[ch * 8 + j] = -INFINITY;
+            for (int j = 0; j < 8; j++) {
+              const float x = fmaf(s8[j] * q8[j], ka, vb);
+              tv[ch * 8 + j] = seen ? x : -INFINITY;
+              past |= tv[ch * 8 + j] > p8[j];
             }
-#pragma unroll
-            for (int j = 0; j < 8; j++) past |= tv[ch * 8 + j] - rs.m[ch * 8 + j] > kMax;
           }
         }
         tc05_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s_free[gg & 1]));
-        const bool move = softmax_any(past);
+        if (__any_sync(0xffffffffu, seen && !whole)) {
+          // keys that some rows see and others do not (causal and window edges)
+          past = false;
+#pragma unroll
+          for (int r = 0; r < GC * 8; r++)
+            if (r < n_ch * 8) {
+              if (!(pos >= rs.lo[g0 + r] && pos < rs.hi[g0 + r])) tv[r] = -INFINITY;
+              past |= tv[r] > rs.past[g0 + r];
+            }
+        }
+        const bool move = group_any(group, past);
         gone = dead[look++ & 1];
         if (gone) break;
         if (move) {
           // new references: a row's largest t over the tile at 2^kTop, where it passed 2^kMax
 #pragma unroll
-          for (int ch = 0; ch < RMAX / 8; ch++) {
-            if (ch * 8 < rp) {
+          for (int ch = 0; ch < GC; ch++) {
+            if (ch < n_ch) {
               float v8[8];
 #pragma unroll
               for (int j = 0; j < 8; j++) v8[j] = tv[ch * 8 + j];
               const float mx = reduce8(v8, [](float x, float y) { return fmaxf(x, y); });
-              if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = mx;
+              if ((lane & 3) == 0) rs.red[quarter][g0 + ch * 8 + (lane >> 2)] = mx;
             }
           }
-          softmax_sync();
-          if (key < rp) {
-            const float mx = fmaxf(fmaxf(rs.red[0][key], rs.red[1][key]), fmaxf(rs.red[2][key], rs.red[3][key]));
-            const float old = rs.m[key], m = mx - old > kMax ? mx - kTop : old;
-            rs.m[key] = m;
-            rs.f[key] = m == old ? 1.f : ex2(old - m);
+          group_sync(group);
+          if (key < n_ch * 8) {
+            const int r = g0 + key;
+            const float mx = fmaxf(fmaxf(rs.red[0][r], rs.red[1][r]), fmaxf(rs.red[2][r], rs.red[3][r]));
+            const float old = rs.m[r], m = mx > rs.past[r] ? mx - kTop : old;
+            rs.m[r] = m;
+            if (m != old) rs.past[r] = m + kMax;
+            rs.f[r] = m == old ? 1.f : ex2(old - m);
           }
-          softmax_sync();
+          group_sync(group);
 #pragma unroll
-          for (int r = 0; r < RMAX; r++)
-            if (r < rp) l[r] *= rs.f[r];
+          for (int r = 0; r < GC * 8; r++)
+            if (r < n_ch * 8) l[r] *= rs.f[g0 + r];
           if (t > 0) {
-            if (!mbar_wait_bounded(smem_u32(p_free), (gg - 1) & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
-            __syncwarp();
+            wait(p_free, gg - 1);
             tc05_fence_after();
+#pragma unroll 1
             for (int col = 0; col < PANELS * TERMS; col++) {
-              const uint32_t to = tmem_o + lanes + (uint32_t)((col / TERMS) * N + (col % TERMS) * rp);
-              for (int ch = 0; ch < rp; ch += 8) {
+              const uint32_t to = tmem_o + lanes + (uint32_t)((col / TERMS) * N + (col % TERMS) * rp + g0);
+#pragma unroll 1
+              for (int ch = 0; ch < n_ch * 8; ch += 8) {
                 float o8[8];
                 tmem_ld8(to + ch, o8);
 #pragma unroll
-                for (int j = 0; j < 8; j++) o8[j] *= rs.f[ch + j];
+                for (int j = 0; j < 8; j++) o8[j] *= rs.f[g0 + ch + j];
                 tmem_st8(to + ch, o8);
               }
             }
@@ -655,56 +715,58 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
           }
         }
         // the probabilities of the tile before have been read
-        if (gg > 0 && !mbar_wait_bounded(smem_u32(p_free), (gg - 1) & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
-        __syncwarp();
-        bool v_nan = false;
+        if (gg > 0) wait(p_free, gg - 1);
         if (!whole) {
           // A key that no row sees must not reach the product: its code bytes may be anything, and 0 * NaN
           // is NaN. Nor may a NaN value reach the rows that do not see its key: there it becomes 0 and the
-          // weight becomes NaN for the rows that do.
-          const bool seen = blk >= 0 && pos >= sg.r.lo && pos < sg.r.len;
+          // weight becomes NaN for the rows that do. Both groups may be at it: one that finds a NaN cleared finds
+          // the note that was made before.
+          bool v_nan = false;
           const int sq = base + (t + 1 < n_tiles ? 2 * t + 2 : 2 * n_tiles - 1), slot = sq % S;
           if (!mbar_wait_bounded(smem_u32(&full[slot]), (sq / S) & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
-#pragma unroll
-          for (int p = 0; p < PANELS; p++)
-#pragma unroll
-            for (int c = 0; c < ROWB / 16; c++) {
-              uint4* at = reinterpret_cast<uint4*>(ring + (size_t)slot * STAGE + p * PANEL + key * ROWB + c * 16);
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (seen) {
-                x = *at;
-                uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                  const uint32_t bad = __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                  v_nan |= bad != 0;
-                  w[i] &= ~bad;
-                }
-              }
-              if (!seen || v_nan) *at = x;
+#pragma unroll 1
+          for (int c = 0; c < HD / 16; c++) {
+            uint4* at = reinterpret_cast<uint4*>(ring + (size_t)slot * STAGE + (c >> 3) * PANEL + key * ROWB + (c & 7) * 16);
+            uint4 x = make_uint4(0, 0, 0, 0), bad = x;
+            if (seen) {
+              x = *at;
+              bad = make_uint4(__vcmpeq4(x.x & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(x.y & 0x7f7f7f7fu, 0x7f7f7f7fu),
+                               __vcmpeq4(x.z & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(x.w & 0x7f7f7f7fu, 0x7f7f7f7fu));
+              if (!(bad.x | bad.y | bad.z | bad.w)) continue;
+              v_nan = true;
+              *reinterpret_cast<volatile int*>(&rs.nan_tile[key]) = gg + 1;
+              __threadfence_block();
             }
-        }
+            *at = make_uint4(x.x & ~bad.x, x.y & ~bad.y, x.z & ~bad.z, x.w & ~bad.w);
+          }
+          __threadfence_block();
+          if (v_nan || *reinterpret_cast<volatile int*>(&rs.nan_tile[key]) == gg + 1) {
 #pragma unroll
-        for (int ch = 0; ch < RMAX / 8; ch++) {
-          if (ch * 8 < rp) {
+            for (int r = 0; r < GC * 8; r++)
+              if (r < n_ch * 8 && tv[r] != -INFINITY) tv[r] = __int_as_float(0x7fffffff);
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int ch = 0; ch < GC; ch++) {
+          if (ch < n_ch) {
+            const float4* mp = reinterpret_cast<const float4*>(&rs.m[g0 + ch * 8]);
+            const float4 m0 = mp[0], m1 = mp[1];
+            const float m8[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
             uint32_t c[4][TERMS];
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
-              float w0 = ex2(tv[ch * 8 + j] - rs.m[ch * 8 + j]), w1 = ex2(tv[ch * 8 + j + 1] - rs.m[ch * 8 + j + 1]);
-              if (v_nan) {
-                if (tv[ch * 8 + j] != -INFINITY) w0 = __int_as_float(0x7fffffff);
-                if (tv[ch * 8 + j + 1] != -INFINITY) w1 = __int_as_float(0x7fffffff);
-              }
+              const float w0 = ex2(tv[ch * 8 + j] - m8[j]), w1 = ex2(tv[ch * 8 + j + 1] - m8[j + 1]);
               l[ch * 8 + j] = fmaf(w0, v_inv, l[ch * 8 + j]);
               l[ch * 8 + j + 1] = fmaf(w1, v_inv, l[ch * 8 + j + 1]);
               split2<TERMS>(w0, w1, c[j / 2]);
             }
 #pragma unroll
             for (int i = 0; i < TERMS; i++) {
-              const int o = i * rp + ch * 8;
+              const int o = i * rp + g0 + ch * 8;
               const uint32_t to = p_row + ((((uint32_t)o >> 4) ^ (key & 7)) << 4) + (o & 8);
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(c[0][i] | (c[1][i] << 16)),
-                           "r"(c[2][i] | (c[3][i] << 16))
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(__byte_perm(c[0][i], c[1][i], 0x5410)),
+                           "r"(__byte_perm(c[2][i], c[3][i], 0x5410))
                            : "memory");
             }
           }
@@ -724,40 +786,39 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
 
       // ---- end of the segment: L over the keys, then O -------------------------------------------------------
 #pragma unroll
-      for (int ch = 0; ch < RMAX / 8; ch++) {
-        if (ch * 8 < rp) {
+      for (int ch = 0; ch < GC; ch++) {
+        if (ch < n_ch) {
           float v8[8];
 #pragma unroll
           for (int j = 0; j < 8; j++) v8[j] = l[ch * 8 + j];
           const float sum = reduce8(v8, [](float x, float y) { return x + y; });
-          if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = sum;
+          if ((lane & 3) == 0) rs.red[quarter][g0 + ch * 8 + (lane >> 2)] = sum;
         }
       }
-      if (!mbar_wait_bounded(smem_u32(p_free), (g - 1) & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
-      __syncwarp();
-      softmax_sync();
+      wait(p_free, g - 1);
+      group_sync(group);
       gone = dead[look++ & 1];
       if (gone) break;
       const bool direct = sg.t0 == 0 && sg.t1 == sg.r.tiles && !a.k_own;
       const size_t slot = (size_t)blockIdx.x + sg.pair;
-      if (key < rp) {
-        const float L = (rs.red[0][key] + rs.red[1][key]) + (rs.red[2][key] + rs.red[3][key]);
-        rs.f[key] = L == 0.f ? 0.f : 1.f / L;
-        if (!direct) a.part_ml[slot * rp + key] = make_float2(rs.m[key], L);
+      if (key < n_ch * 8) {
+        const int r = g0 + key;
+        const float L = (rs.red[0][r] + rs.red[1][r]) + (rs.red[2][r] + rs.red[3][r]);
+        rs.f[r] = L == 0.f ? 0.f : 1.f / L;
+        if (!direct) a.part_ml[slot * rp + r] = make_float2(rs.m[r], L);
       }
-      softmax_sync();
+      group_sync(group);
       tc05_fence_after();
+#pragma unroll 1
+      for (int pc = 0; pc < PANELS * n_ch; pc++) {
+        const int p = PANELS == 1 ? 0 : pc / n_ch, ch = (pc - p * n_ch) * 8 + g0, d = p * 128 + key;
+        float o8[8];
+        tmem_sum8<TERMS>(tmem_o + lanes + (uint32_t)(p * N + ch), rp, o8);
+        if (key < HD) {
 #pragma unroll
-      for (int p = 0; p < PANELS; p++) {
-        const int d = p * 128 + key;
-        for (int ch = 0; ch < rows; ch += 8) {
-          float o8[8];
-          tmem_sum8<TERMS>(tmem_o + lanes + (uint32_t)(p * N + ch), rp, o8);
-          if (key < HD) {
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-              const int r = ch + j;
-              if (r >= rows) break;
+          for (int j = 0; j < 8; j++) {
+            const int r = ch + j;
+            if (r < rows) {
               if (direct) {
                 const int row = sg.r.row0 + (r0 + r) / a.grp, head = sg.head * a.grp + (r0 + r) % a.grp;
                 row_store(static_cast<T*>(a.out) + row * a.o_row + head * a.o_head + d, o8[j] * rs.f[r]);
@@ -769,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
         }
       }
       tc05_fence_before();
-      softmax_sync();                                  // rs belongs to the next segment now
+      group_sync(group);                               // the group's part of rs belongs to the next segment now
     }
   }
 
@@ -784,6 +845,20 @@ __global__ void __launch_bounds__(kThreads, RMAX <= 40 ? 2 : 1)
 // ---- the second kernel: join the pieces of a row, own rows, output; one warp per (request, head, row) --------
 constexpr int kJoinWarps = 4;
 
+template <int N>
+__device__ __forceinline__ void load_floats(const float* p, float (&v)[N]) {
+  if constexpr (N == 2) {
+    const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+    v[0] = x.x, v[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(p + i));
+      v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+    }
+  }
+}
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
   constexpr int PER = HD / 32;                         // columns per lane
@@ -794,7 +869,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
   const int r = (int)(task % a.p.rc), pair = (int)(task / a.p.rc);
   const int chunk = pair % a.p.chunks, head = pair / a.p.chunks % a.n_kv, b = pair / a.p.chunks / a.n_kv;
   if (b >= a.n_req) return;
-  const Request rq = request_of(a, b);
+  const Request rq = request_of(a, read_request(a, b));
   const int rr = chunk * a.p.rc + r;
   if (rr >= rq.n * a.grp) return;
   const int i = rr / a.grp, qh = head * a.grp + rr % a.grp, row = rq.row0 + i;
@@ -817,13 +892,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
     for (int c = 0; c < PER; c++) o[c] = fmaf(v[c], sn, o[c] * so);
     m = mn;
   };
-  for (int c = c0; c <= c1; c++) {
-    const size_t at = ((size_t)c + pair) * a.p.rp + r;
-    const float2 ml = __ldcg(&a.part_ml[at]);
-    float v[PER];
+  constexpr int kAtOnce = 8;                           // pieces in flight
+  for (int c = c0; c <= c1; c += kAtOnce) {
+    float2 ml[kAtOnce];
+    float v[kAtOnce][PER];
 #pragma unroll
-    for (int j = 0; j < PER; j++) v[j] = __ldcg(a.part_o + at * HD + lane * PER + j);
-    if (ml.x != kUnset) take(ml.x, ml.y, v);
+    for (int u = 0; u < kAtOnce; u++) {
+      ml[u] = make_float2(kUnset, 0.f);
+      if (c + u <= c1) {
+        const size_t at = ((size_t)(c + u) + pair) * a.p.rp + r;
+        ml[u] = __ldcg(&a.part_ml[at]);
+        load_floats<PER>(a.part_o + at * HD + lane * PER, v[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; u++)
+      if (ml[u].x != kUnset) take(ml[u].x, ml[u].y, v[u]);
   }
   if (a.k_own) {
     float q[PER];
@@ -849,12 +933,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
   for (int c = 0; c < PER; c++) row_store(out + c, o[c] * inv);
 }
 
-template <typename T, int HD, int RMAX>
+template <typename T, int HD, int GROUPS, int GC>
 cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
   static std::atomic<int> smem_set[kMaxDevices];
-  cudaError_t e = ensure_smem_limit(cache_attn_kernel<T, HD, RMAX>, a.p.smem, smem_set);
+  const auto kernel = cache_attn_kernel<T, HD, GROUPS, GC>;
+  cudaError_t e = ensure_smem_limit(kernel, a.p.smem, smem_set);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(cache_attn_kernel<T, HD, RMAX>, dim3(a.grid), dim3(kThreads), a.p.smem, s, a, kmap, vmap);
+  e = launch_pdl(kernel, dim3(a.grid), dim3(threads_of(GROUPS)), a.p.smem, s, a, kmap, vmap);
   if (e != cudaSuccess) return e;
   const long long tasks = (long long)a.n_req * a.n_kv * a.p.chunks * a.p.rc;
   return launch_pdl(cache_attn_join_kernel<T, HD>, dim3((unsigned)((tasks + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, s, a);
@@ -862,9 +947,9 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtens
 
 template <typename T, int HD>
 cudaError_t launch_rows(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
-  if (a.p.rp <= 8) return launch<T, HD, 8>(a, kmap, vmap, s);
-  if (a.p.rp <= 40) return launch<T, HD, 40>(a, kmap, vmap, s);
-  if constexpr (__is_same(T, __nv_bfloat16)) return launch<T, HD, 64>(a, kmap, vmap, s);
+  if (a.p.rp <= 8) return launch<T, HD, 1, 1>(a, kmap, vmap, s);
+  if (a.p.rp <= 48) return launch<T, HD, 2, 3>(a, kmap, vmap, s);
+  if constexpr (__is_same(T, __nv_bfloat16)) return launch<T, HD, 2, 4>(a, kmap, vmap, s);
   return cudaErrorInvalidValue;
 }
 
