@@ -31,7 +31,8 @@ cudaError_t launch_cache_append(int dtype, const CacheAppendArgs& a, cudaStream_
 // KV head are cut into chunks of rc rows, each padded to rp columns and carried as `terms` e4m3 terms.
 struct CacheAttnPlan {
   int terms;               // e4m3 terms of a query or probability: 2 (bf16), 3 (f16)
-  int chunks, rc, rp, n;   // n: MMA columns, terms * rp rounded up to 16 (<= 128)
+  int chunks, rc, rp;
+  int ns, n;               // MMA columns: rp, and terms * rp, rounded up to 16 (n <= 128)
   int ctas_per_sm, stages, tmem_cols;
   size_t smem;
 };

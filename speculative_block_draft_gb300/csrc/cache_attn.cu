@@ -10,9 +10,10 @@
 // Keys are the tensor-memory lanes of S, so a thread owns a key: few rows fill every lane, a row's
 // softmax needs no exchange between threads while its reference stays (below), and a thread's
 // probabilities are contiguous bytes of the second product's operand. Queries and probabilities
-// are not e4m3 values, so both enter as sums of e4m3 terms side by side as further columns: a value's
-// nearest code, the nearest code of what that leaves, and so on. Two terms hold bf16's 8 significant
-// bits, three f16's 11. The terms' columns of S are added when it is read, those of O at the end.
+// are not e4m3 values, so both enter as sums of e4m3 terms: a value's nearest code, the nearest code of what that
+// leaves, and so on. Two terms hold bf16's 8 significant bits, three f16's 11. The first product adds the
+// terms of Q up in one accumulator; those of P are further columns of the second one (cheaper: an MMA of up to
+// 64 columns takes the time of one of 64), added when O is read.
 //
 //   t_ij = s_ij * q_scale_i * k_scale * scale * log2(e) + log2(v_scale)    (scales of the key's block)
 //   w_ij = 2^(t_ij - m_i)                       = p_ij * v_scale / 2^m_i
@@ -41,13 +42,17 @@ namespace dfl {
 namespace {
 
 constexpr int kTile = 128;               // keys per tile
-// Warp 0: copies, warp 1: MMAs, then one or two groups of four softmax warps. The groups share a tile's keys and
-// split its query rows: each has its own rows' references, barrier and part of the output.
-__host__ __device__ constexpr int threads_of(int groups) { return 64 + 128 * groups; }
+constexpr int kThreads = 256;            // warp 0: copies, 1: MMAs, 2: later queries, 3: none; warps 4-7: softmax
+constexpr int kSoftmax0 = 128;           // first softmax thread
+// With two CTAs per SM a thread starts with 128 registers; the softmax warps take over part of the others'.
+constexpr int kStartRegs = 128, kOtherRegs = 96, kSoftmaxRegs = 160;
+static_assert(kOtherRegs + kSoftmaxRegs <= 2 * kStartRegs, "the shares come out of what the CTA was launched with");
+constexpr int kConstRing = 16;           // tiles whose key constants are kept
 constexpr int kMaxStages = 12;
 constexpr int kPBytes = kTile * 128;     // probabilities: 128 keys x up to 128 columns
 constexpr float kTop = 5.f, kMax = 8.75f;
-constexpr float kUnset = -1e30f;         // reference of a row that has seen no key
+constexpr float kUnset = -1e30f;         // reference of a piece whose row has seen no key
+constexpr int kRowsOfTwo = 40;           // most rows with two CTAs per SM (registers)
 constexpr int kRowArrays = 64;           // rows of the per-row arrays in shared memory
 
 __device__ __forceinline__ float row_f(__half v) { return __half2float(v); }
@@ -180,23 +185,49 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
 // The sum of `TERMS` groups of 8 columns, `step` columns apart.
 template <int TERMS>
 __device__ __forceinline__ void tmem_sum8(uint32_t taddr, uint32_t step, float (&v)[8]) {
-  uint32_t r[8], s[8];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(s[0]),
-        "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]), "=r"(s[7])
-      : "r"(taddr), "r"(taddr + step)
-      : "memory");
+  tmem_ld8(taddr, v);
 #pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]) + __uint_as_float(s[i]);
-  if constexpr (TERMS == 3) {
+  for (int t = 1; t < TERMS; t++) {
     float w[8];
-    tmem_ld8(taddr + 2 * step, w);
+    tmem_ld8(taddr + t * step, w);
 #pragma unroll
     for (int i = 0; i < 8; i++) v[i] += w[i];
   }
+}
+
+// The same load in two halves: the registers may be used once tmem_wait8 has returned.
+__device__ __forceinline__ void tmem_start8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait8(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+
+// Two fp32 lanes per instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8]) {
@@ -216,17 +247,17 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Barrier of the four warps of softmax group `id`; `any` returns whether any thread's predicate holds.
-__device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id + 1) : "memory"); }
-__device__ __forceinline__ bool group_any(int id, bool v) {
+// Barrier of the four softmax warps; `any` returns whether any thread's predicate holds.
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.aligned.pred q, %2, 128, p;\n\t"
+      "barrier.cta.red.or.aligned.pred q, 1, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)v), "r"(id + 1)
+      : "r"((uint32_t)v)
       : "memory");
   return r != 0;
 }
@@ -275,67 +306,136 @@ __device__ __forceinline__ float row_scale(float amax) {
   return __int_as_float((max(k, kMinScaleExp) + 127) << 23);
 }
 
-// Two values as TERMS pairs of e4m3 codes (low byte: x), in f16: |x|, |y| <= 448. The first rounding, to
-// f16, is at the last term's level (2^-12).
+// Four values as TERMS words of four e4m3 codes (the first in the low byte), from f16: magnitudes <= 448. The
+// rounding to f16 is at the last term's level (2^-12).
 template <int TERMS>
-__device__ __forceinline__ void split2(float x, float y, uint32_t (&c)[TERMS]) {
-  __half2 v = __floats2half2_rn(x, y);
+__device__ __forceinline__ void split4(float2 x, float2 y, uint32_t (&c)[TERMS]) {
+  uint32_t u, v;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(x.y), "f"(x.x));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(y.y), "f"(y.x));
 #pragma unroll
   for (int t = 0; t < TERMS; t++) {
-    const __half2_raw raw = *reinterpret_cast<const __half2_raw*>(&v);
-    const __nv_fp8x2_storage_t code = __nv_cvt_halfraw2_to_fp8x2(raw, __NV_SATFINITE, __NV_E4M3);
-    c[t] = code;
     if (t + 1 < TERMS) {
-      const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(code, __NV_E4M3);
-      v = __hsub2(v, *reinterpret_cast<const __half2*>(&back));
+      asm("{.reg .b16 p, q;\n\t.reg .b32 b, d;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f16x2 p, %1;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f16x2 q, %2;\n\t"
+          "mov.b32 %0, {p, q};\n\t"
+          "cvt.rn.f16x2.e4m3x2 b, p;\n\t"
+          "cvt.rn.f16x2.e4m3x2 d, q;\n\t"
+          "sub.rn.f16x2 %1, %1, b;\n\t"
+          "sub.rn.f16x2 %2, %2, d;}"
+          : "=r"(c[t]), "+r"(u), "+r"(v));
+    } else {
+      asm("{.reg .b16 p, q;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f16x2 p, %1;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f16x2 q, %2;\n\t"
+          "mov.b32 %0, {p, q};}"
+          : "=r"(c[t]) : "r"(u), "r"(v));
     }
   }
 }
 
 // ---- shared memory -----------------------------------------------------------------------------------
 struct alignas(16) RowState {            // per query row of the CTA's chunk
-  float m[kRowArrays];                   // reference
-  float past[kRowArrays];                // reference + kMax: a larger t moves it
-  float qs[kRowArrays];                  // the row's query scale
+  float4 key[kConstRing][kTile / 16];    // per tile and block: k_scale * scale * log2(e), log2(v_scale), 1 / v_scale, there or not
+  float neg_m[kRowArrays];               // minus the reference
+  float qs[2][kRowArrays];               // the row's query scale; by turns for the segments, as the queries
   float f[kRowArrays];                   // factor of a moved reference; 1 / L at the end
   float red[4][kRowArrays];              // per softmax warp: maxima, sums
   int lo[kRowArrays], hi[kRowArrays];    // visible positions
-  int nan_tile[kTile];                   // per key: 1 + the last tile whose value had a NaN that was cleared
+  int unset[kRowArrays];                 // the row has seen no key (its reference is 0)
+  int64_t out[kRowArrays];               // its element offset in the output
 };
 
 __host__ __device__ constexpr int panels_of(int hd) { return hd == 256 ? 2 : 1; }
 __host__ __device__ constexpr int stage_bytes(int hd) { return kTile * hd; }
 
 __host__ __device__ inline size_t attn_fixed_smem(int hd, int n, int n_req) {
-  return (size_t)n * 128 * panels_of(hd) + kPBytes + sizeof(RowState) + (2 * kMaxStages + 8) * 8 + 64 + 20 * (size_t)(n_req + 1);
+  return (size_t)2 * n * 128 * panels_of(hd) + kPBytes + sizeof(RowState) + (2 * kMaxStages + 12) * 8 + 64 + 20 * (size_t)(n_req + 1);
 }
 
 // ---- the first kernel ----------------------------------------------------------------------------------
-// GROUPS softmax groups of at most 8 * GC rows each.
-template <typename T, int HD, int GROUPS, int GC>
-__global__ void __launch_bounds__(threads_of(GROUPS), GC <= 3 ? 2 : 1)
+// The queries of a segment as e4m3 terms in shared memory (rows of 128 bytes, swizzled as the MMA reads them; a
+// second panel for the columns from 128), by `threads` threads. A row is scaled so that its largest value lies
+// in (224, 448]; qs gets the scale.
+template <typename T, int HD, int TERMS>
+__device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Segment& sg, uint8_t* q_s, float* qs, int tid, int threads) {
+  constexpr int kPerRow = HD / 8, kAhead = 5;          // lanes of a row; rows in flight per lane
+  const int rp = a.p.rp, N = a.p.n, r0 = sg.chunk * a.p.rc, rows = min(a.p.rc, sg.r.n * a.grp - r0);
+  const int c8 = (tid % kPerRow) * 8, at_once = threads / kPerRow;
+  for (int first = tid / kPerRow; first < rp; first += kAhead * at_once) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; u++) {
+      const int r = first + u * at_once;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int row = sg.r.row0 + (r0 + r) / a.grp, head = sg.head * a.grp + (r0 + r) % a.grp;
+        v[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + row * a.q_row + head * a.q_head + c8);
+      }
+    }
+#pragma unroll 1
+    for (int u = 0; u < kAhead; u++) {
+      const int r = first + u * at_once;
+      const uint4 now = v[0];                          // the rows move down: one copy of this code
+#pragma unroll
+      for (int w = 0; w + 1 < kAhead; w++) v[w] = v[w + 1];
+      if (r - tid / kPerRow >= rp) break;              // no lane of the warp has a row
+      const T* e = reinterpret_cast<const T*>(&now);
+      float x[8], amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        x[j] = row_f(e[j]);
+        const float m = fabsf(x[j]);
+        if (m <= 3.402823466e38f) amax = fmaxf(amax, m);
+        else x[j] = __int_as_float(0x7fffffff);        // an infinite query has no softmax
+      }
+#pragma unroll
+      for (int o = kPerRow / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const float sc = row_scale(amax), inv = __uint_as_float((254u << 23) - __float_as_uint(sc));
+      if (r < rp) {
+        uint32_t c[2][TERMS];
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+          split4<TERMS>(make_float2(x[4 * j] * inv, x[4 * j + 1] * inv), make_float2(x[4 * j + 2] * inv, x[4 * j + 3] * inv), c[j]);
+#pragma unroll
+        for (int t = 0; t < TERMS; t++) {
+          const int n = t * rp + r;
+          uint8_t* to = q_s + (c8 >> 7) * (N * 128) + n * 128 + ((((c8 & 127) >> 4) ^ (n & 7)) << 4) + (c8 & 8);
+          *reinterpret_cast<uint2*>(to) = make_uint2(c[0][t], c[1][t]);
+        }
+        if (c8 == 0) qs[r] = sc;
+      }
+    }
+  }
+}
+
+// RMAX: most query rows of a chunk.
+template <typename T, int HD, int RMAX>
+__global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
     cache_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
-  constexpr int kThreads = threads_of(GROUPS), kWarps = kThreads / 32;
-  constexpr int TERMS = sizeof(T) == 2 && __is_same(T, __nv_bfloat16) ? 2 : 3;
+  constexpr int TERMS = __is_same(T, __nv_bfloat16) ? 2 : 3;
   constexpr int PANELS = panels_of(HD), STAGE = stage_bytes(HD);
   constexpr int ROWB = HD < 128 ? HD : 128;            // bytes of a key in a panel
   constexpr int PANEL = kTile * 128;                   // bytes between panels (HD = 256)
+  constexpr int CH = RMAX / 8;                         // chunks of 8 rows
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  const int S = a.p.stages, N = a.p.n, rp = a.p.rp;
+  const int S = a.p.stages, N = a.p.n, NS = a.p.ns, rp = a.p.rp;
+  const int q_bytes = N * 128 * PANELS;
   uint8_t* ring = sm;
-  uint8_t* q_s = ring + (size_t)S * STAGE;
-  uint8_t* p_s = q_s + N * 128 * PANELS;
+  uint8_t* q_s = ring + (size_t)S * STAGE;             // two buffers, by turns for the segments
+  uint8_t* p_s = q_s + 2 * q_bytes;
   RowState& rs = *reinterpret_cast<RowState*>(p_s + kPBytes);
   uint64_t* bars = reinterpret_cast<uint64_t*>(&rs + 1);
   uint64_t *full = bars, *empty = bars + kMaxStages, *s_full = bars + 2 * kMaxStages, *s_free = s_full + 2, *q_full = s_full + 4,
-           *p_full = s_full + 5, *p_free = s_full + 6;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 8);
-  // Set when a softmax wait gave up: per group, and by turns for the stretches between two points where all of its
-  // threads look (just behind a barrier), so that all of them see the same and leave together
-  volatile int* dead_flags = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* scan = reinterpret_cast<int*>(tmem_slot + 5);   // warp sums
+           *q_free = s_full + 6, *p_full = s_full + 8, *p_free = s_full + 9, *drained = s_full + 10;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 12);
+  // Set when a softmax wait gave up, by turns for the stretches between two points where all softmax threads look
+  // (just behind a barrier), so that all of them see the same and leave together
+  volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* scan = reinterpret_cast<int*>(tmem_slot + 3);   // warp sums
   int4* words = reinterpret_cast<int4*>(tmem_slot + 16);
   int* before = reinterpret_cast<int*>(words + a.n_req);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -346,15 +446,15 @@ __global__ void __launch_bounds__(threads_of(GROUPS), GC <= 3 ? 2 : 1)
       mbar_init(smem_u32(&empty[i]), 1);
     }
     for (int i = 0; i < 2; i++) {
-      mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&s_free[i]), 4 * GROUPS);
+      mbar_init(smem_u32(&s_full[i]), 2);              // the MMAs, and the warp that issued them
+      mbar_init(smem_u32(&s_free[i]), 4);
+      mbar_init(smem_u32(&q_full[i]), 1);
+      mbar_init(smem_u32(&q_free[i]), 2);              // the MMAs, and the softmax warps
     }
-    mbar_init(smem_u32(q_full), 4 * GROUPS);
-    mbar_init(smem_u32(p_full), 4 * GROUPS);
+    mbar_init(smem_u32(p_full), 4);
     mbar_init(smem_u32(p_free), 1);
-    mbar_init(smem_u32(s_full + 7), 1);
-    for (int i = 0; i < 4; i++) dead_flags[i] = 0;
-    for (int i = 0; i < kTile; i++) rs.nan_tile[i] = 0;
+    mbar_init(smem_u32(drained), 1);
+    dead[0] = dead[1] = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -391,7 +491,7 @@ __global__ void __launch_bounds__(threads_of(GROUPS), GC <= 3 ? 2 : 1)
     __syncthreads();
     int at = s - mine;
 #pragma unroll
-    for (int w = 0; w < kWarps; w++) at += w < warp ? scan[w] : 0;
+    for (int w = 0; w < kThreads / 32; w++) at += w < warp ? scan[w] : 0;
     for (int j = 0; j < per; j++)
       if (b0 + j < a.n_req) {
         const int u = before[b0 + j];
@@ -417,54 +517,88 @@ __global__ void __launch_bounds__(threads_of(GROUPS), GC <= 3 ? 2 : 1)
     walk.b = lo;
   }
   // Ring order: K of a tile one step ahead of V of the one before: K0 K1 V0 K2 V1 .. V(n-1) per segment.
-  const uint32_t tmem_o = tmem + 2 * N;
+  const uint32_t tmem_o = tmem + 2 * NS;
   Segment sg;
 
+  constexpr bool kSplitRegs = RMAX == kRowsOfTwo;
+  if (warp < 4) {
+  if (kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 0) {
-    // ---- copies: one per block of the tile (and 128-byte panel), each by a lane of its own -------------
-    int seq = 0;
+    // ---- copies: one per block of the tile (and 128-byte panel), each by a lane of its own, which also leaves the
+    // block's scales for the softmax -----------------------------------------------------------------------
+    int seq = 0, g = 0;
     bool ok = true;
     const int nb = kTile >> a.log_t;
     while (ok && walk.next(a, before, words, sg)) {
-      auto entry_of = [&](int t) {                     // this lane's block of tile t, -1: nothing to copy
-        const int idx = (sg.r.s0 >> a.log_t) + t * nb + lane;
-        if (lane >= nb || t >= sg.t1 || ((long long)idx << a.log_t) >= sg.r.len) return -1;
-        const int e = *(a.table + (int64_t)sg.r.req * a.table_blocks + idx % a.table_blocks);
-        return in_bounds(e >= 0 && e < a.n_blocks, a.err) ? e : -1;
+      const int* table = a.table + (int64_t)sg.r.req * a.table_blocks;
+      const int idx0 = (sg.r.s0 >> a.log_t) + lane;
+      auto entry_of = [&](int t) {                     // this lane's block of tile t (as it is), -1: none
+        const int idx = idx0 + t * nb;
+        return lane < nb && t < sg.t1 && ((long long)idx << a.log_t) < sg.r.len ? table[idx % a.table_blocks] : -1;
       };
-      auto copy = [&](const CUtensorMap* map, int e) {
+      struct Block {
+        int e;
+        float ks, vs;
+      };
+      auto block_of = [&](int e) {                     // -1 if it is not there; its scales
+        Block b{-1, 0.f, 0.f};
+        if (e != -1 && in_bounds(e >= 0 && e < a.n_blocks, a.err)) {
+          b.e = e;
+          b.ks = a.k_scale[(int64_t)e * a.n_kv + sg.head];
+          b.vs = a.v_scale[(int64_t)e * a.n_kv + sg.head];
+        }
+        return b;
+      };
+      auto copy = [&](const CUtensorMap* map, const Block& b, bool key) {
         const int slot = seq % S;
         if (seq >= S) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&empty[slot]), (seq / S + 1) & 1, a.err, kErrTimeoutCache));
         if (!ok) return;
+        // The softmax has read the constants that these replace: the ring of tiles is deeper than the copies run
+        // ahead. This stage was free, so the scores of the tile S / 2 back were issued, and the two score
+        // buffers let that happen when those of two tiles before it had been read, its constants with them.
+        if (key && lane < nb) {
+          float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (b.e >= 0) {
+            scale_terms(fmaxf(b.vs, __int_as_float((kMinScaleExp + 127) << 23)), c.y, c.z);
+            c.x = b.ks * a.scale_log2;
+            c.w = 1.f;
+          }
+          rs.key[g % kConstRing][lane] = c;
+        }
         const uint32_t bar = smem_u32(&full[slot]);
-        const int n = __popc(__ballot_sync(0xffffffffu, e >= 0));
+        const int n = __popc(__ballot_sync(0xffffffffu, b.e >= 0));
+        __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * ((uint32_t)HD << a.log_t));
         __syncwarp();
-        if (e >= 0) {
+        if (b.e >= 0) {
           const uint32_t dst = smem_u32(ring + (size_t)slot * STAGE) + ((uint32_t)(lane * ROWB) << a.log_t);
 #pragma unroll
-          for (int p = 0; p < PANELS; p++) tma_load_5d(dst + p * PANEL, map, p * 128, 0, sg.head, e, a.layer, bar);
+          for (int p = 0; p < PANELS; p++) tma_load_5d(dst + p * PANEL, map, p * 128, 0, sg.head, b.e, a.layer, bar);
         }
         __syncwarp();
         seq++;
+        if (key) g++;
       };
-      int cur = entry_of(sg.t0), nxt = entry_of(sg.t0 + 1);
-      copy(&kmap, cur);
+      // entries two and three tiles ahead, scales one ahead
+      Block cur = block_of(entry_of(sg.t0)), nxt = block_of(entry_of(sg.t0 + 1));
+      int far = entry_of(sg.t0 + 2);
+      copy(&kmap, cur, true);
       for (int t = sg.t0; ok && t < sg.t1; t++) {
-        const int far = entry_of(t + 2);
-        if (t + 1 < sg.t1) copy(&kmap, nxt);
-        if (ok) copy(&vmap, cur);
+        const Block after = block_of(far);
+        far = entry_of(t + 3);
+        if (t + 1 < sg.t1) copy(&kmap, nxt, true);
+        if (ok) copy(&vmap, cur, false);
         cur = nxt;
-        nxt = far;
+        nxt = after;
       }
     }
     // no copy may be in flight when the CTA leaves: the last fill of every stage has landed
     for (int j = max(0, seq - S); j < seq; j++) mbar_wait_bounded(smem_u32(&full[j % S]), (j / S) & 1, nullptr, 0);
   } else if (warp == 1) {
     // ---- MMAs ---------------------------------------------------------------------------------------------
-    const uint32_t id_s = idesc_e4m3(N, false), id_o = idesc_e4m3(N, true);
+    const uint32_t id_s = idesc_e4m3(NS, false), id_o = idesc_e4m3(N, true);
     const uint32_t ring_a = smem_u32(ring);
-    const uint64_t qd = smem_desc(smem_u32(q_s), 16, 1024, 2), pd = smem_desc(smem_u32(p_s), 16, 1024, 2);
+    const uint64_t qd0 = smem_desc(smem_u32(q_s), 16, 1024, 2), pd = smem_desc(smem_u32(p_s), 16, 1024, 2);
     int base = 0, g = 0, n_seg = 0, pv_done = 0;       // g: tiles so far
     bool ok = true;
     auto wait = [&](uint64_t* bar, int parity) {
@@ -472,8 +606,8 @@ __global__ void __launch_bounds__(threads_of(GROUPS), GC <= 3 ? 2 : 1)
     };
     while (ok && walk.next(a, before, words, sg)) {
       const int n = sg.t1 - sg.t0;
-      ok = wait(q_full, n_seg);
-      n_seg++;
+      const uint64_t qd = qd0 + (uint64_t)((n_seg & 1) * (q_bytes >> 4));
+      ok = wait(&q_full[n_seg & 1], n_seg >> 1);
       auto scores = [&](int t) {                       // tile t of the segment
         const int sq = base + (t == 0 ? 0 : 2 * t - 1), slot = sq % S, gg = g + t;
         ok = ok && wait(&full[slot], sq / S);
@@ -481,15 +615,19 @@ __global__ void __launch_bounds__(threads_of(GROUPS), GC <= 3 ? 2 : 1)
         if (!ok) return;
         tc05_fence_after();
         const uint64_t kd = HD == 64 ? smem_desc(ring_a + slot * STAGE, 16, 512, 4) : smem_desc(ring_a + slot * STAGE, 16, 1024, 2);
-        const uint32_t d = tmem + (uint32_t)((gg & 1) * N);
+        const uint32_t d = tmem + (uint32_t)((gg & 1) * NS);
 #pragma unroll
         for (int ks = 0; ks < HD / 32; ks++) {
           const uint64_t ka = kd + (uint64_t)((ks / 4) * (PANEL >> 4) + (ks % 4) * 2);
           const uint64_t qa = qd + (uint64_t)((ks / 4) * (N * 8) + (ks % 4) * 2);
-          umma_e4m3_warp(d, ka, qa, id_s, ks > 0);
+#pragma unroll
+          for (int i = 0; i < TERMS; i++) umma_e4m3_warp(d, ka, qa + (uint64_t)(i * rp * 8), id_s, ks > 0 || i > 0);
         }
         umma_commit_warp(smem_u32(&empty[slot]));
         umma_commit_warp(smem_u32(&s_full[gg & 1]));
+        if (t + 1 == n) umma_commit_warp(smem_u32(&q_free[n_seg & 1]));
+        if (lane == 0) mbar_arrive(smem_u32(&s_full[gg & 1]));   // passes the copy warp's constants on
+        __syncwarp();
       };
       if (ok) scores(0);
       for (int t = 0; ok && t < n; t++) {
@@ -512,23 +650,35 @@ __global__ void __launch_bounds__(threads_of(GROUPS), GC <= 3 ? 2 : 1)
       }
       base += 2 * n;
       g += n;
+      n_seg++;
     }
     // nothing of this CTA may still run on the tensor core when its memory is freed. After a wait that gave up
     // there may be scores without a probability product: their commits have a barrier of their own
     if (pv_done > 0) mbar_wait_bounded(smem_u32(p_free), (uint32_t)(pv_done - 1) & 1, a.err, kErrTimeoutCache);
     if (!ok) {
-      umma_commit_warp(smem_u32(s_full + 7));
-      mbar_wait_bounded(smem_u32(s_full + 7), 0, nullptr, 0);
+      umma_commit_warp(smem_u32(drained));
+      mbar_wait_bounded(smem_u32(drained), 0, nullptr, 0);
     }
+  } else if (warp == 2) {
+    // ---- queries of the segments after the first, while the one before is at work ---------------------------
+    bool ok = true;
+    for (int k = 0; ok && walk.next(a, before, words, sg); k++) {
+      if (k == 0) continue;
+      if (k >= 2) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&q_free[k & 1]), ((k >> 1) + 1) & 1, a.err, kErrTimeoutCache));
+      if (!ok) break;
+      prepare_queries<T, HD, TERMS>(a, sg, q_s + (k & 1) * q_bytes, rs.qs[k & 1], lane, 32);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&q_full[k & 1]));
+    }
+  }
   } else {
+    if (kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax ------------------------------------------------------------------------------------------
-    const int group = GROUPS == 1 ? 0 : (warp - 2) >> 2, quarter = warp & 3, key = quarter * 32 + lane;
+    const int quarter = warp & 3, key = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t p_row = smem_u32(p_s) + key * 128;
-    volatile int* dead = dead_flags + 2 * group;
-    const int half = (rp / 8 + GROUPS - 1) / GROUPS;                      // chunks of 8 rows: this group's first, and one past
-    const int ch0 = group * half, n_ch = min(half, rp / 8 - ch0), g0 = ch0 * 8;
-    int base = 0, g = 0, look = 0;
+    int base = 0, g = 0, look = 0, n_seg = 0;
     bool gone = false;
     auto wait = [&](uint64_t* bar, int parity) {
       if (!mbar_wait_bounded(smem_u32(bar), (uint32_t)parity & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
@@ -536,238 +686,191 @@ __global__ void __launch_bounds__(threads_of(GROUPS), GC <= 3 ? 2 : 1)
     };
     while (!gone && walk.next(a, before, words, sg)) {
       const int n_tiles = sg.t1 - sg.t0, r0 = sg.chunk * a.p.rc, rows = min(a.p.rc, sg.r.n * a.grp - r0);
-      // the group's rows: visible range, query as e4m3 terms
-      if (key < n_ch * 8) {
-        const int r = g0 + key;
-        rs.m[r] = kUnset;
-        rs.past[r] = kUnset;
+      if (key < rp) {
+        rs.neg_m[key] = 0.f;
+        rs.unset[key] = key < rows;
         int lo = 0, hi = 0;
-        if (r < rows) row_range(a, sg.r, (r0 + r) / a.grp, lo, hi);
-        rs.lo[r] = lo;
-        rs.hi[r] = hi;
-      }
-      {
-        constexpr int kPerRow = HD / 8, kRowsAtOnce = 128 / kPerRow, kPasses = (GC * 8 + kRowsAtOnce - 1) / kRowsAtOnce;
-        const int c8 = (key % kPerRow) * 8;
-        uint4 v[kPasses];
-#pragma unroll
-        for (int u = 0; u < kPasses; u++) {
-          const int r = g0 + key / kPerRow + u * kRowsAtOnce;
-          v[u] = make_uint4(0, 0, 0, 0);
-          if (r < rows && r < g0 + n_ch * 8) {
-            const int row = sg.r.row0 + (r0 + r) / a.grp, head = sg.head * a.grp + (r0 + r) % a.grp;
-            v[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + row * a.q_row + head * a.q_head + c8);
-          }
+        if (key < rows) {
+          const int i = (r0 + key) / a.grp;
+          row_range(a, sg.r, i, lo, hi);
+          rs.out[key] = (sg.r.row0 + i) * a.o_row + (sg.head * a.grp + (r0 + key) - i * a.grp) * a.o_head;
         }
-#pragma unroll 1
-        for (int u = 0; u < kPasses; u++) {
-          const int r = g0 + key / kPerRow + u * kRowsAtOnce;
-          const uint4 now = v[0];                      // the passes move down: one copy of this code
-#pragma unroll
-          for (int w = 0; w + 1 < kPasses; w++) v[w] = v[w + 1];
-          const T* e = reinterpret_cast<const T*>(&now);
-          float x[8], amax = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; j++) {
-            x[j] = row_f(e[j]);
-            const float m = fabsf(x[j]);
-            if (m <= 3.402823466e38f) amax = fmaxf(amax, m);
-            else x[j] = __int_as_float(0x7fffffff);    // an infinite query has no softmax
-          }
-#pragma unroll
-          for (int o = kPerRow / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          const float sc = row_scale(amax), inv = __uint_as_float((254u << 23) - __float_as_uint(sc));
-          if (r < g0 + n_ch * 8) {
-            uint32_t c[4][TERMS];
-#pragma unroll
-            for (int j = 0; j < 4; j++) split2<TERMS>(x[2 * j] * inv, x[2 * j + 1] * inv, c[j]);
-#pragma unroll
-            for (int t = 0; t < TERMS; t++) {
-              const int n = t * rp + r;
-              uint8_t* to = q_s + (c8 >> 7) * (N * 128) + n * 128 + ((((c8 & 127) >> 4) ^ (n & 7)) << 4) + (c8 & 8);
-              *reinterpret_cast<uint2*>(to) = make_uint2(c[0][t] | (c[1][t] << 16), c[2][t] | (c[3][t] << 16));
-            }
-            if (c8 == 0) rs.qs[r] = sc;
-          }
-        }
+        rs.lo[key] = lo;
+        rs.hi[key] = hi;
       }
-      fence_proxy_async();
+      const float* row_qs = rs.qs[n_seg & 1];
+      if (n_seg == 0) {
+        prepare_queries<T, HD, TERMS>(a, sg, q_s, rs.qs[0], threadIdx.x - kSoftmax0, 128);
+        fence_proxy_async();
+      } else {
+        wait(&q_full[n_seg & 1], n_seg >> 1);
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(q_full));
-      group_sync(group);
+      softmax_sync();
+      if (n_seg == 0 && threadIdx.x == kSoftmax0) mbar_arrive(smem_u32(&q_full[0]));
+      __syncwarp();
 
       int lo_all, hi_all, dummy;                       // keys that every row sees
       row_range(a, sg.r, r0 / a.grp, dummy, hi_all);
       row_range(a, sg.r, (r0 + rows - 1) / a.grp, lo_all, dummy);
-      // this thread's key of tile t: block number, then its scales (one and two tiles ahead)
-      auto block_of = [&](int t) {
-        const long long pos = (long long)sg.r.s0 + (long long)t * kTile + key;
-        if (t >= sg.t1 || pos >= sg.r.len) return -1;
-        const int e = *(a.table + (int64_t)sg.r.req * a.table_blocks + (int)(pos >> a.log_t) % a.table_blocks);
-        return e >= 0 && e < a.n_blocks ? e : -1;
-      };
-      int blk = block_of(sg.t0), blk_next = block_of(sg.t0 + 1);
-      auto scales = [&](int e, float& ks, float& vs) {
-        ks = 0.f, vs = 1.f;
-        if (e >= 0) {
-          ks = *(a.k_scale + (int64_t)e * a.n_kv + sg.head);
-          vs = *(a.v_scale + (int64_t)e * a.n_kv + sg.head);
-        }
-      };
-      float ks, vs;
-      scales(blk, ks, vs);
-      float l[GC * 8];
+      bool unset_any = true;                           // some row has seen no key
+      float2 l[CH * 4];
 #pragma unroll
-      for (int r = 0; r < GC * 8; r++) l[r] = 0.f;
+      for (int r = 0; r < CH * 4; r++) l[r] = make_float2(0.f, 0.f);
+      int pos = sg.r.s0 + sg.t0 * kTile + key;
 
 #pragma unroll 1
-      for (int t = 0; t < n_tiles; t++) {
+      for (int t = 0; t < n_tiles; t++, pos += kTile) {
         const int gg = g + t;
-        const int blk_far = block_of(sg.t0 + t + 2);
-        float ks_next, vs_next;
-        scales(blk_next, ks_next, vs_next);
-        const int pos = sg.r.s0 + (sg.t0 + t) * kTile + key;
-        const float ka = ks * a.scale_log2;
-        float vb, v_inv;
-        scale_terms(fmaxf(vs, __int_as_float((kMinScaleExp + 127) << 23)), vb, v_inv);
-        const bool seen = blk >= 0 && pos >= sg.r.lo && pos < sg.r.len;      // by some row
-        const bool whole = seen && pos >= lo_all && pos < hi_all;            // by every row
         wait(&s_full[gg & 1], gg >> 1);
         tc05_fence_after();
-        float tv[GC * 8];
-        bool past = false;
-        const uint32_t ts = tmem + lanes + (uint32_t)((gg & 1) * N + g0);
+        const float4 kc = rs.key[gg % kConstRing][key >> a.log_t];
+        const float2 ka = make_float2(kc.x, kc.x), vb2 = make_float2(kc.y, kc.y), inv2 = make_float2(kc.z, kc.z);
+        const bool seen = kc.w != 0.f && pos >= sg.r.lo && pos < sg.r.len;   // by some row
+        const bool whole = seen && pos >= lo_all && pos < hi_all;             // by every row
+        // x = t - m of this key for each row
+        float2 x[CH * 4];
+        float top = -INFINITY;
+        const uint32_t ts = tmem + lanes + (uint32_t)((gg & 1) * NS);
+        uint32_t s8[2][8];
+        tmem_start8(ts, s8[0]);
 #pragma unroll
-        for (int ch = 0; ch < GC; ch++) {
-          if (ch < n_ch) {
-            float s8[8];
-            tmem_sum8<TERMS>(ts + ch * 8, rp, s8);
-            const float4* qs = reinterpret_cast<const float4*>(&rs.qs[g0 + ch * 8]);
-            const float4* pt = reinterpret_cast<const float4*>(&rs.past[g0 + ch * 8]);
-            const float4 q0 = qs[0], q1 = qs[1], p0 = pt[0], p1 = pt[1];
-            const float q8[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-            const float p8[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+        for (int ch = 0; ch < CH; ch++) {
+          if (ch * 8 < rp) {
+            const float4* qp = reinterpret_cast<const float4*>(row_qs + ch * 8);
+            const float4* mp = reinterpret_cast<const float4*>(&rs.neg_m[ch * 8]);
+            const float4 q0 = qp[0], q1 = qp[1], m0 = mp[0], m1 = mp[1];
+            tmem_wait8(s8[ch & 1]);
+            if ((ch + 1) * 8 < rp) tmem_start8(ts + ch * 8 + 8, s8[(ch + 1) & 1]);
+            const float2 q2[4] = {{q0.x, q0.y}, {q0.z, q0.w}, {q1.x, q1.y}, {q1.z, q1.w}};
+            const float2 m2[4] = {{m0.x, m0.y}, {m0.z, m0.w}, {m1.x, m1.y}, {m1.z, m1.w}};
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-              const float x = fmaf(s8[j] * q8[j], ka, vb);
-              tv[ch * 8 + j] = seen ? x : -INFINITY;
-              past |= tv[ch * 8 + j] > p8[j];
+            for (int j = 0; j < 4; j++) {
+              const float2 sc = make_float2(__uint_as_float(s8[ch & 1][2 * j]), __uint_as_float(s8[ch & 1][2 * j + 1]));
+              const float2 v = fma2(mul2(sc, q2[j]), ka, add2(vb2, m2[j]));
+              x[ch * 4 + j] = v;
+              top = fmaxf(top, fmaxf(v.x, v.y));
             }
           }
         }
         tc05_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s_free[gg & 1]));
-        if (__any_sync(0xffffffffu, seen && !whole)) {
-          // keys that some rows see and others do not (causal and window edges)
-          past = false;
+        if (__any_sync(0xffffffffu, !whole)) {
+          // keys that no row sees, or some rows and others not (ends, causal and window edges)
+          top = -INFINITY;
 #pragma unroll
-          for (int r = 0; r < GC * 8; r++)
-            if (r < n_ch * 8) {
-              if (!(pos >= rs.lo[g0 + r] && pos < rs.hi[g0 + r])) tv[r] = -INFINITY;
-              past |= tv[r] > rs.past[g0 + r];
+          for (int r = 0; r < CH * 4; r++)
+            if (r * 2 < rp) {
+              const int2 lo = *reinterpret_cast<const int2*>(&rs.lo[2 * r]), hi = *reinterpret_cast<const int2*>(&rs.hi[2 * r]);
+              if (!(seen && (whole || (pos >= lo.x && pos < hi.x)))) x[r].x = -INFINITY;
+              if (!(seen && (whole || (pos >= lo.y && pos < hi.y)))) x[r].y = -INFINITY;
+              top = fmaxf(top, fmaxf(x[r].x, x[r].y));
             }
         }
-        const bool move = group_any(group, past);
+        const bool move = softmax_any(top > kMax || unset_any);
         gone = dead[look++ & 1];
         if (gone) break;
         if (move) {
-          // new references: a row's largest t over the tile at 2^kTop, where it passed 2^kMax
+          // new references: a row's largest t over the tile at 2^kTop, where it passed 2^kMax or is the first
 #pragma unroll
-          for (int ch = 0; ch < GC; ch++) {
-            if (ch < n_ch) {
+          for (int ch = 0; ch < CH; ch++) {
+            if (ch * 8 < rp) {
               float v8[8];
 #pragma unroll
-              for (int j = 0; j < 8; j++) v8[j] = tv[ch * 8 + j];
-              const float mx = reduce8(v8, [](float x, float y) { return fmaxf(x, y); });
-              if ((lane & 3) == 0) rs.red[quarter][g0 + ch * 8 + (lane >> 2)] = mx;
+              for (int j = 0; j < 4; j++) v8[2 * j] = x[ch * 4 + j].x, v8[2 * j + 1] = x[ch * 4 + j].y;
+              const float mx = reduce8(v8, [](float p, float q) { return fmaxf(p, q); });
+              if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = mx;
             }
           }
-          group_sync(group);
-          if (key < n_ch * 8) {
-            const int r = g0 + key;
-            const float mx = fmaxf(fmaxf(rs.red[0][r], rs.red[1][r]), fmaxf(rs.red[2][r], rs.red[3][r]));
-            const float old = rs.m[r], m = mx > rs.past[r] ? mx - kTop : old;
-            rs.m[r] = m;
-            if (m != old) rs.past[r] = m + kMax;
-            rs.f[r] = m == old ? 1.f : ex2(old - m);
+          softmax_sync();
+          bool still = false;
+          if (key < rp) {
+            const float mx = fmaxf(fmaxf(rs.red[0][key], rs.red[1][key]), fmaxf(rs.red[2][key], rs.red[3][key]));
+            const bool first = rs.unset[key] && mx > -INFINITY;
+            const float by = first || mx > kMax ? mx - kTop : 0.f;        // the reference grows by this
+            rs.red[0][key] = by;
+            rs.f[key] = first ? 0.f : ex2(-by);
+            rs.neg_m[key] -= by;
+            if (first) rs.unset[key] = 0;
+            still = rs.unset[key];
           }
-          group_sync(group);
+          unset_any = softmax_any(still);
 #pragma unroll
-          for (int r = 0; r < GC * 8; r++)
-            if (r < n_ch * 8) l[r] *= rs.f[g0 + r];
+          for (int r = 0; r < CH * 4; r++)
+            if (r * 2 < rp) {
+              const float2 by = *reinterpret_cast<const float2*>(&rs.red[0][2 * r]), f = *reinterpret_cast<const float2*>(&rs.f[2 * r]);
+              x[r] = make_float2(x[r].x - by.x, x[r].y - by.y);
+              l[r] = mul2(l[r], f);
+            }
           if (t > 0) {
             wait(p_free, gg - 1);
             tc05_fence_after();
 #pragma unroll 1
-            for (int col = 0; col < PANELS * TERMS; col++) {
-              const uint32_t to = tmem_o + lanes + (uint32_t)((col / TERMS) * N + (col % TERMS) * rp + g0);
+            for (int c = 0; c < PANELS * TERMS; c++) {
+              const uint32_t to = tmem_o + lanes + (uint32_t)((c / TERMS) * N + (c % TERMS) * rp);
 #pragma unroll 1
-              for (int ch = 0; ch < n_ch * 8; ch += 8) {
+              for (int ch = 0; ch < rp; ch += 8) {
                 float o8[8];
                 tmem_ld8(to + ch, o8);
 #pragma unroll
-                for (int j = 0; j < 8; j++) o8[j] *= rs.f[g0 + ch + j];
+                for (int j = 0; j < 8; j++) o8[j] *= rs.f[ch + j];
                 tmem_st8(to + ch, o8);
               }
             }
             tmem_wait_st();
           }
+          softmax_sync();                              // red has been read
         }
         // the probabilities of the tile before have been read
         if (gg > 0) wait(p_free, gg - 1);
         if (!whole) {
           // A key that no row sees must not reach the product: its code bytes may be anything, and 0 * NaN
           // is NaN. Nor may a NaN value reach the rows that do not see its key: there it becomes 0 and the
-          // weight becomes NaN for the rows that do. Both groups may be at it: one that finds a NaN cleared finds
-          // the note that was made before.
+          // weight becomes NaN for the rows that do.
           bool v_nan = false;
           const int sq = base + (t + 1 < n_tiles ? 2 * t + 2 : 2 * n_tiles - 1), slot = sq % S;
           if (!mbar_wait_bounded(smem_u32(&full[slot]), (sq / S) & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
 #pragma unroll 1
           for (int c = 0; c < HD / 16; c++) {
             uint4* at = reinterpret_cast<uint4*>(ring + (size_t)slot * STAGE + (c >> 3) * PANEL + key * ROWB + (c & 7) * 16);
-            uint4 x = make_uint4(0, 0, 0, 0), bad = x;
+            uint4 w = make_uint4(0, 0, 0, 0), bad = w;
             if (seen) {
-              x = *at;
-              bad = make_uint4(__vcmpeq4(x.x & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(x.y & 0x7f7f7f7fu, 0x7f7f7f7fu),
-                               __vcmpeq4(x.z & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(x.w & 0x7f7f7f7fu, 0x7f7f7f7fu));
+              w = *at;
+              bad = make_uint4(__vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu),
+                               __vcmpeq4(w.z & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(w.w & 0x7f7f7f7fu, 0x7f7f7f7fu));
               if (!(bad.x | bad.y | bad.z | bad.w)) continue;
               v_nan = true;
-              *reinterpret_cast<volatile int*>(&rs.nan_tile[key]) = gg + 1;
-              __threadfence_block();
             }
-            *at = make_uint4(x.x & ~bad.x, x.y & ~bad.y, x.z & ~bad.z, x.w & ~bad.w);
+            *at = make_uint4(w.x & ~bad.x, w.y & ~bad.y, w.z & ~bad.z, w.w & ~bad.w);
           }
-          __threadfence_block();
-          if (v_nan || *reinterpret_cast<volatile int*>(&rs.nan_tile[key]) == gg + 1) {
+          if (v_nan) {
 #pragma unroll
-            for (int r = 0; r < GC * 8; r++)
-              if (r < n_ch * 8 && tv[r] != -INFINITY) tv[r] = __int_as_float(0x7fffffff);
+            for (int r = 0; r < CH * 4; r++)
+              if (r * 2 < rp) {
+                if (x[r].x != -INFINITY) x[r].x = __int_as_float(0x7fffffff);
+                if (x[r].y != -INFINITY) x[r].y = __int_as_float(0x7fffffff);
+              }
           }
         }
         __syncwarp();
 #pragma unroll
-        for (int ch = 0; ch < GC; ch++) {
-          if (ch < n_ch) {
-            const float4* mp = reinterpret_cast<const float4*>(&rs.m[g0 + ch * 8]);
-            const float4 m0 = mp[0], m1 = mp[1];
-            const float m8[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-            uint32_t c[4][TERMS];
+        for (int ch = 0; ch < CH; ch++) {
+          if (ch * 8 < rp) {
+            float2 w[4];
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              const float w0 = ex2(tv[ch * 8 + j] - m8[j]), w1 = ex2(tv[ch * 8 + j + 1] - m8[j + 1]);
-              l[ch * 8 + j] = fmaf(w0, v_inv, l[ch * 8 + j]);
-              l[ch * 8 + j + 1] = fmaf(w1, v_inv, l[ch * 8 + j + 1]);
-              split2<TERMS>(w0, w1, c[j / 2]);
+            for (int j = 0; j < 4; j++) {
+              w[j] = make_float2(ex2(x[ch * 4 + j].x), ex2(x[ch * 4 + j].y));
+              l[ch * 4 + j] = fma2(w[j], inv2, l[ch * 4 + j]);
             }
+            uint32_t c[2][TERMS];
+            split4<TERMS>(w[0], w[1], c[0]);
+            split4<TERMS>(w[2], w[3], c[1]);
 #pragma unroll
             for (int i = 0; i < TERMS; i++) {
-              const int o = i * rp + g0 + ch * 8;
+              const int o = i * rp + ch * 8;
               const uint32_t to = p_row + ((((uint32_t)o >> 4) ^ (key & 7)) << 4) + (o & 8);
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(__byte_perm(c[0][i], c[1][i], 0x5410)),
-                           "r"(__byte_perm(c[2][i], c[3][i], 0x5410))
-                           : "memory");
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(c[0][i]), "r"(c[1][i]) : "memory");
             }
           }
         }
@@ -775,10 +878,6 @@ __global__ void __launch_bounds__(threads_of(GROUPS), GC <= 3 ? 2 : 1)
         tc05_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(p_full));
-        blk = blk_next;
-        blk_next = blk_far;
-        ks = ks_next;
-        vs = vs_next;
       }
       base += 2 * n_tiles;
       g += n_tiles;
@@ -786,51 +885,51 @@ __global__ void __launch_bounds__(threads_of(GROUPS), GC <= 3 ? 2 : 1)
 
       // ---- end of the segment: L over the keys, then O -------------------------------------------------------
 #pragma unroll
-      for (int ch = 0; ch < GC; ch++) {
-        if (ch < n_ch) {
+      for (int ch = 0; ch < CH; ch++) {
+        if (ch * 8 < rp) {
           float v8[8];
 #pragma unroll
-          for (int j = 0; j < 8; j++) v8[j] = l[ch * 8 + j];
-          const float sum = reduce8(v8, [](float x, float y) { return x + y; });
-          if ((lane & 3) == 0) rs.red[quarter][g0 + ch * 8 + (lane >> 2)] = sum;
+          for (int j = 0; j < 4; j++) v8[2 * j] = l[ch * 4 + j].x, v8[2 * j + 1] = l[ch * 4 + j].y;
+          const float sum = reduce8(v8, [](float p, float q) { return p + q; });
+          if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = sum;
         }
       }
       wait(p_free, g - 1);
-      group_sync(group);
+      softmax_sync();
       gone = dead[look++ & 1];
       if (gone) break;
+      if (threadIdx.x == kSoftmax0) mbar_arrive(smem_u32(&q_free[n_seg & 1]));
       const bool direct = sg.t0 == 0 && sg.t1 == sg.r.tiles && !a.k_own;
       const size_t slot = (size_t)blockIdx.x + sg.pair;
-      if (key < n_ch * 8) {
-        const int r = g0 + key;
-        const float L = (rs.red[0][r] + rs.red[1][r]) + (rs.red[2][r] + rs.red[3][r]);
-        rs.f[r] = L == 0.f ? 0.f : 1.f / L;
-        if (!direct) a.part_ml[slot * rp + r] = make_float2(rs.m[r], L);
+      if (key < rp) {
+        const float L = (rs.red[0][key] + rs.red[1][key]) + (rs.red[2][key] + rs.red[3][key]);
+        rs.f[key] = L == 0.f ? 0.f : 1.f / L;
+        if (!direct) a.part_ml[slot * rp + key] = make_float2(rs.unset[key] ? kUnset : -rs.neg_m[key], L);
       }
-      group_sync(group);
+      softmax_sync();
       tc05_fence_after();
+      float* part = a.part_o + slot * rp * HD + key;
+      T* out = static_cast<T*>(a.out) + key;
 #pragma unroll 1
-      for (int pc = 0; pc < PANELS * n_ch; pc++) {
-        const int p = PANELS == 1 ? 0 : pc / n_ch, ch = (pc - p * n_ch) * 8 + g0, d = p * 128 + key;
-        float o8[8];
-        tmem_sum8<TERMS>(tmem_o + lanes + (uint32_t)(p * N + ch), rp, o8);
-        if (key < HD) {
+      for (int p = 0; p < PANELS; p++) {
+#pragma unroll 1
+        for (int ch = 0; ch < rows; ch += 8) {
+          float o8[8];
+          tmem_sum8<TERMS>(tmem_o + lanes + (uint32_t)(p * N + ch), rp, o8);
+          if (key < HD) {
 #pragma unroll
-          for (int j = 0; j < 8; j++) {
-            const int r = ch + j;
-            if (r < rows) {
-              if (direct) {
-                const int row = sg.r.row0 + (r0 + r) / a.grp, head = sg.head * a.grp + (r0 + r) % a.grp;
-                row_store(static_cast<T*>(a.out) + row * a.o_row + head * a.o_head + d, o8[j] * rs.f[r]);
-              } else {
-                a.part_o[(slot * rp + r) * HD + d] = o8[j];
+            for (int j = 0; j < 8; j++) {
+              if (ch + j < rows) {
+                if (direct) row_store(out + rs.out[ch + j] + p * 128, o8[j] * rs.f[ch + j]);
+                else part[(ch + j) * HD + p * 128] = o8[j];
               }
             }
           }
         }
       }
       tc05_fence_before();
-      group_sync(group);                               // the group's part of rs belongs to the next segment now
+      softmax_sync();                                  // rs belongs to the next segment now
+      n_seg++;
     }
   }
 
@@ -933,13 +1032,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
   for (int c = 0; c < PER; c++) row_store(out + c, o[c] * inv);
 }
 
-template <typename T, int HD, int GROUPS, int GC>
+template <typename T, int HD, int RMAX>
 cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
   static std::atomic<int> smem_set[kMaxDevices];
-  const auto kernel = cache_attn_kernel<T, HD, GROUPS, GC>;
-  cudaError_t e = ensure_smem_limit(kernel, a.p.smem, smem_set);
+  cudaError_t e = ensure_smem_limit(cache_attn_kernel<T, HD, RMAX>, a.p.smem, smem_set);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kernel, dim3(a.grid), dim3(threads_of(GROUPS)), a.p.smem, s, a, kmap, vmap);
+  if (RMAX == kRowsOfTwo) {   // the softmax warps would wait for registers that the CTA does not have
+    static const int regs = [] {
+      cudaFuncAttributes at{};
+      return cudaFuncGetAttributes(&at, cache_attn_kernel<T, HD, RMAX>) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs < kStartRegs) return cudaErrorInvalidConfiguration;
+  }
+  e = launch_pdl(cache_attn_kernel<T, HD, RMAX>, dim3(a.grid), dim3(kThreads), a.p.smem, s, a, kmap, vmap);
   if (e != cudaSuccess) return e;
   const long long tasks = (long long)a.n_req * a.n_kv * a.p.chunks * a.p.rc;
   return launch_pdl(cache_attn_join_kernel<T, HD>, dim3((unsigned)((tasks + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, s, a);
@@ -947,9 +1052,9 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtens
 
 template <typename T, int HD>
 cudaError_t launch_rows(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
-  if (a.p.rp <= 8) return launch<T, HD, 1, 1>(a, kmap, vmap, s);
-  if (a.p.rp <= 48) return launch<T, HD, 2, 3>(a, kmap, vmap, s);
-  if constexpr (__is_same(T, __nv_bfloat16)) return launch<T, HD, 2, 4>(a, kmap, vmap, s);
+  if (a.p.rp <= 8) return launch<T, HD, 8>(a, kmap, vmap, s);
+  if (a.p.rp <= kRowsOfTwo) return launch<T, HD, kRowsOfTwo>(a, kmap, vmap, s);
+  if constexpr (__is_same(T, __nv_bfloat16)) return launch<T, HD, 64>(a, kmap, vmap, s);
   return cudaErrorInvalidValue;
 }
 
@@ -974,14 +1079,15 @@ CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req) 
   p.rc = (rows + p.chunks - 1) / p.chunks;
   p.rp = (p.rc + 7) / 8 * 8;
   p.n = (p.terms * p.rp + 15) / 16 * 16;
-  const int cols = (2 + panels_of(hd)) * p.n;
+  p.ns = (p.rp + 15) / 16 * 16;
+  const int cols = 2 * p.ns + panels_of(hd) * p.n;
   p.tmem_cols = 32;
   while (p.tmem_cols < cols) p.tmem_cols *= 2;
   const size_t fixed = attn_fixed_smem(hd, p.n, n_req) + 1024;
   constexpr size_t kPerSm = 227 * 1024;
-  // two CTAs per SM where tensor memory allows it and each still holds four key or value tiles
+  // two CTAs per SM where registers and tensor memory allow it and each still holds four key or value tiles
   const size_t half = kPerSm / 2 - 1024;
-  p.ctas_per_sm = p.tmem_cols <= 256 && fixed + 4 * (size_t)stage_bytes(hd) <= half ? 2 : 1;
+  p.ctas_per_sm = p.rp <= kRowsOfTwo && p.tmem_cols <= 256 && fixed + 4 * (size_t)stage_bytes(hd) <= half ? 2 : 1;
   const size_t room = (p.ctas_per_sm == 2 ? half : kPerSm) - fixed;
   p.stages = (int)std::min<size_t>(kMaxStages, room / stage_bytes(hd));
   p.smem = fixed + (size_t)p.stages * stage_bytes(hd);
