@@ -42,6 +42,7 @@ struct CacheAttnArgs {
   const float *k_scale, *v_scale;                  // of the call's layer
   int layer, n_blocks, n_kv, hd, log_t, grp;
   int n_req, n_rows, max_q, table_rows, table_blocks, causal, window;
+  int held;                                        // tokens that a table row can name
   const int32_t *requests, *lens, *table, *row_start;
   const void *q, *k_own, *v_own;
   void* out;

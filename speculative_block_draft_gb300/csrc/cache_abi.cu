@@ -49,11 +49,11 @@ bool valid(const dflash_cache_config* c) {
 }
 
 // Rows of attention pieces that a call within the limits can leave: one per query row, padded, of each
-// (request, KV head), and the CTAs' own. A chunk of rows is padded to less than 8 + 1 more, and there are at
-// least 40 rows in every chunk but one; a CTA's chunk holds at most 64 rows, and an SM two CTAs.
+// (request, KV head), and the CTAs' own. A chunk of rows is padded by at most 23 (41 rows as 64) and a share of one
+// row, and there is one for every 40 rows at most; a CTA's chunk holds at most 64 rows, and an SM two CTAs.
 int64_t piece_rows(const dflash_cache_config& f, int n_sm) {
   const int64_t rows = (int64_t)(f.n_q_heads / f.n_kv_heads) * f.max_q;
-  return (int64_t)2 * n_sm * 64 + (int64_t)f.max_requests * f.n_kv_heads * (rows + 9 * ((rows + 39) / 40));
+  return (int64_t)2 * n_sm * 64 + (int64_t)f.max_requests * f.n_kv_heads * (rows + 24 * ((rows + 39) / 40));
 }
 
 size_t round_256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -230,6 +230,7 @@ int dflash_cache_attention(dflash_cache* c, const dflash_attention* p, void* str
   a.max_q = p->max_q;
   a.table_rows = p->table_rows;
   a.table_blocks = p->table_blocks;
+  a.held = (int)std::min<int64_t>((int64_t)p->table_blocks << c->log_t, 0x7fffffff);
   a.causal = p->causal;
   a.window = p->window;
   a.requests = p->requests;

@@ -42,7 +42,7 @@ namespace dfl {
 namespace {
 
 constexpr int kTile = 128;               // keys per tile
-constexpr int kThreads = 256;            // warp 0: copies, 1: MMAs, 2: later queries, 3: none; warps 4-7: softmax
+constexpr int kThreads = 256;            // warp 0: copies, 1: MMAs, 2 and 3: queries; warps 4-7: softmax
 constexpr int kSoftmax0 = 128;           // first softmax thread
 // With two CTAs per SM a thread starts with 128 registers; the softmax warps take over part of the others'.
 constexpr int kStartRegs = 128, kOtherRegs = 96, kSoftmaxRegs = 160;
@@ -74,19 +74,19 @@ struct Request {
   int chunks;
 };
 
-// First visible position of row i of the request, and one past its last (cached keys).
+// First visible position of row i of the request, and one past its last (cached keys). Lengths end below 2^31 - 2^16,
+// so positions of rows fit 32 bits.
 __device__ __forceinline__ void row_range(const CacheAttnArgs& a, const Request& r, int i, int& lo, int& hi) {
-  const long long held = (long long)a.table_blocks << a.log_t;   // a ring holds the last ones
-  long long l = max(0LL, (long long)r.len - held), h = r.len;
+  lo = max(0, r.len - a.held);                          // a ring holds the last ones
+  hi = r.len;
   if (a.causal) {
-    const long long at = a.k_own ? (long long)r.len + i : (long long)r.len - r.n + i;
-    h = min(h, at + 1);
-    if (a.window > 0) l = max(l, at + 1 - a.window);
+    const int at = a.k_own ? r.len + i : r.len - r.n + i;
+    hi = min(hi, at + 1);
+    if (a.window > 0) lo = max(lo, at + 1 - a.window);
   } else if (a.window > 0) {
-    l = max(l, (long long)r.len - a.window);
+    lo = max(lo, r.len - a.window);
   }
-  lo = (int)l;
-  hi = (int)max(h, 0LL);
+  hi = max(hi, 0);
 }
 
 // What a call says about request b: first query row, query rows, cached tokens, table row.
@@ -113,7 +113,7 @@ __device__ __forceinline__ Request request_of(const CacheAttnArgs& a, int4 w) {
   row_range(a, r, 0, r.lo, hi);
   r.s0 = r.lo & ~((1 << a.log_t) - 1);
   r.tiles = r.n > 0 && r.lo < r.len ? (r.len - r.s0 + kTile - 1) / kTile : 0;
-  r.chunks = (r.n * a.grp + a.p.rc - 1) / a.p.rc;
+  r.chunks = a.p.chunks == 1 ? 1 : (r.n * a.grp + a.p.rc - 1) / a.p.rc;
   return r;
 }
 
@@ -127,6 +127,17 @@ struct Segment {
   int t0, t1;
 };
 
+// A place in the ring of key and value tiles, in order.
+struct Ring {
+  int slot = 0, fill = 0;                 // fill: how often the slot has been filled before
+  __device__ void next(int n) {
+    if (++slot == n) {
+      slot = 0;
+      fill++;
+    }
+  }
+};
+
 struct Walk {
   int u, u_end, b;
   __device__ bool next(const CacheAttnArgs& a, const int* before, const int4* words, Segment& s) {
@@ -134,11 +145,11 @@ struct Walk {
     while (u >= before[b + 1]) b++;
     s.b = b;
     s.r = request_of(a, words[b]);
-    const int rem = u - before[b], p = rem / s.r.tiles;
-    s.head = p / s.r.chunks;
-    s.chunk = p % s.r.chunks;
+    const unsigned rem = u - before[b], tiles = s.r.tiles, chunks = s.r.chunks, p = rem / tiles;
+    s.head = p / chunks;
+    s.chunk = p - s.head * chunks;
     s.pair = (b * a.n_kv + s.head) * a.p.chunks + s.chunk;
-    s.t0 = rem - p * s.r.tiles;
+    s.t0 = rem - p * tiles;
     s.t1 = min(s.r.tiles, s.t0 + (u_end - u));
     u += s.t1 - s.t0;
     return true;
@@ -170,32 +181,7 @@ __device__ __forceinline__ void umma_e4m3_warp(uint32_t d_tmem, uint64_t a_desc,
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
-  uint32_t r[8];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
-}
-
-// The sum of `TERMS` groups of 8 columns, `step` columns apart.
-template <int TERMS>
-__device__ __forceinline__ void tmem_sum8(uint32_t taddr, uint32_t step, float (&v)[8]) {
-  tmem_ld8(taddr, v);
-#pragma unroll
-  for (int t = 1; t < TERMS; t++) {
-    float w[8];
-    tmem_ld8(taddr + t * step, w);
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] += w[i];
-  }
-}
-
-// The same load in two halves: the registers may be used once tmem_wait8 has returned.
+// A load of 8 columns: the registers may be used once tmem_wait8 has returned.
 __device__ __forceinline__ void tmem_start8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -262,6 +248,35 @@ __device__ __forceinline__ bool softmax_any(bool v) {
   return r != 0;
 }
 
+// Wait for phase `parity` of an mbarrier for at most a second; on giving up, set the error bit and return false. (As
+// mbar_wait_bounded, in few instructions: the loops here have a dozen waits.)
+__device__ __forceinline__ bool wait_bar(const uint64_t* bar, int parity, unsigned* err) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u64 t0, t1;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 t0, %%globaltimer;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 t1, %%globaltimer;\n\t"
+      "sub.u64 t1, t1, t0;\n\t"
+      "setp.lt.u64 q, t1, 1000000000;\n\t"
+      "@q bra AGAIN;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"((uint32_t)parity & 1)
+      : "memory");
+  if (!ok && err) atomicOr(err, kErrTimeoutCache);
+  return ok;
+}
+// The same by a converged warp, for all its lanes.
+__device__ __forceinline__ bool wait_bar_warp(const uint64_t* bar, int parity, unsigned* err) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, err));
+}
+
 // log2 and reciprocal of a scale, exact for the powers of two that the append writes.
 __device__ __forceinline__ void scale_terms(float v, float& lg, float& inv) {
   const uint32_t u = __float_as_uint(v);
@@ -274,27 +289,17 @@ __device__ __forceinline__ void scale_terms(float v, float& lg, float& inv) {
   }
 }
 
-// 8 values per lane -> over the warp: lane l returns the reduction of value (l >> 2) & 7 (lanes of a
-// quad agree). Nine shuffles instead of forty.
+// Sums or maxima over the warp of 8 values per lane: lane l returns that of value (l >> 2) & 7 (lanes of a quad agree).
+// Nine shuffles instead of forty (and a redux.sync per value took 70 cycles each).
 template <typename F>
 __device__ __forceinline__ float reduce8(const float (&v)[8], F f) {
   const int lane = threadIdx.x & 31;
   float a[4], b[2];
-  const bool hi = lane & 16;
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const float mine = hi ? v[i + 4] : v[i], send = hi ? v[i] : v[i + 4];
-    a[i] = f(mine, __shfl_xor_sync(0xffffffffu, send, 16));
-  }
-  const bool hi2 = lane & 8;
+  for (int i = 0; i < 4; i++) a[i] = f(lane & 16 ? v[i + 4] : v[i], __shfl_xor_sync(0xffffffffu, lane & 16 ? v[i] : v[i + 4], 16));
 #pragma unroll
-  for (int i = 0; i < 2; i++) {
-    const float mine = hi2 ? a[i + 2] : a[i], send = hi2 ? a[i] : a[i + 2];
-    b[i] = f(mine, __shfl_xor_sync(0xffffffffu, send, 8));
-  }
-  const bool hi3 = lane & 4;
-  const float mine = hi3 ? b[1] : b[0], send = hi3 ? b[0] : b[1];
-  float c = f(mine, __shfl_xor_sync(0xffffffffu, send, 4));
+  for (int i = 0; i < 2; i++) b[i] = f(lane & 8 ? a[i + 2] : a[i], __shfl_xor_sync(0xffffffffu, lane & 8 ? a[i] : a[i + 2], 8));
+  float c = f(lane & 4 ? b[1] : b[0], __shfl_xor_sync(0xffffffffu, lane & 4 ? b[0] : b[1], 4));
   c = f(c, __shfl_xor_sync(0xffffffffu, c, 2));
   return f(c, __shfl_xor_sync(0xffffffffu, c, 1));
 }
@@ -335,6 +340,35 @@ __device__ __forceinline__ void split4(float2 x, float2 y, uint32_t (&c)[TERMS])
   }
 }
 
+// The nearest value of 4 significant bits (1 + 3, as e4m3 has) to x >= 0, halves up; a NaN becomes 0.
+__device__ __forceinline__ float four_bits(float x) { return __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xfff00000u); }
+
+// Eight weights (>= 0, <= 448) as TERMS groups of eight e4m3 codes. In fp32: the conversions from fp32 are single
+// instructions, and taking the four bits of a term off is exact. A weight below 2^-6 meets the step of the subnormal
+// codes, 2^-9, in more than one term: it is off by at most 2 * 2^-10.
+template <int TERMS>
+__device__ __forceinline__ void split8(const float2 (&w)[4], uint2 (&c)[TERMS]) {
+  float2 r[4] = {w[0], w[1], w[2], w[3]};
+#pragma unroll
+  for (int t = 0; t < TERMS; t++) {
+    float2 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      h[i] = r[i];
+      if (t + 1 < TERMS) {
+        h[i] = make_float2(four_bits(r[i].x), four_bits(r[i].y));
+        r[i] = add2(r[i], make_float2(-h[i].x, -h[i].y));
+      }
+    }
+    asm("{.reg .b16 p, q;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 p, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 q, %4, %3;\n\tmov.b32 %0, {p, q};}"
+        : "=r"(c[t].x) : "f"(h[0].x), "f"(h[0].y), "f"(h[1].x), "f"(h[1].y));
+    asm("{.reg .b16 p, q;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 p, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 q, %4, %3;\n\tmov.b32 %0, {p, q};}"
+        : "=r"(c[t].y) : "f"(h[2].x), "f"(h[2].y), "f"(h[3].x), "f"(h[3].y));
+  }
+}
+
 // ---- shared memory -----------------------------------------------------------------------------------
 struct alignas(16) RowState {            // per query row of the CTA's chunk
   float4 key[kConstRing][kTile / 16];    // per tile and block: k_scale * scale * log2(e), log2(v_scale), 1 / v_scale, there or not
@@ -342,11 +376,15 @@ struct alignas(16) RowState {            // per query row of the CTA's chunk
   float qs[2][kRowArrays];               // the row's query scale; by turns for the segments, as the queries
   float f[kRowArrays];                   // factor of a moved reference; 1 / L at the end
   float red[4][kRowArrays];              // per softmax warp: maxima, sums
+  uint32_t high[4];                      // per softmax warp: chunks of rows with a value above kMax
   int lo[kRowArrays], hi[kRowArrays];    // visible positions
   int unset[kRowArrays];                 // the row has seen no key (its reference is 0)
   int64_t out[kRowArrays];               // its element offset in the output
 };
 
+// MMA columns of the scores and of the weights (multiples of 16)
+__host__ __device__ constexpr int score_columns(int rp) { return (rp + 15) / 16 * 16; }
+__host__ __device__ constexpr int weight_columns(int terms, int rp) { return (terms * rp + 15) / 16 * 16; }
 __host__ __device__ constexpr int panels_of(int hd) { return hd == 256 ? 2 : 1; }
 __host__ __device__ constexpr int stage_bytes(int hd) { return kTile * hd; }
 
@@ -358,12 +396,13 @@ __host__ __device__ inline size_t attn_fixed_smem(int hd, int n, int n_req) {
 // The queries of a segment as e4m3 terms in shared memory (rows of 128 bytes, swizzled as the MMA reads them; a
 // second panel for the columns from 128), by `threads` threads. A row is scaled so that its largest value lies
 // in (224, 448]; qs gets the scale.
-template <typename T, int HD, int TERMS>
+template <typename T, int HD, int TERMS, int RP>
 __device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Segment& sg, uint8_t* q_s, float* qs, int tid, int threads) {
   constexpr int kPerRow = HD / 8, kAhead = 5;          // lanes of a row; rows in flight per lane
-  const int rp = a.p.rp, N = a.p.n, r0 = sg.chunk * a.p.rc, rows = min(a.p.rc, sg.r.n * a.grp - r0);
+  constexpr int N = weight_columns(TERMS, RP);
+  const int r0 = sg.chunk * a.p.rc, rows = min(a.p.rc, sg.r.n * a.grp - r0);
   const int c8 = (tid % kPerRow) * 8, at_once = threads / kPerRow;
-  for (int first = tid / kPerRow; first < rp; first += kAhead * at_once) {
+  for (int first = tid / kPerRow; first < RP; first += kAhead * at_once) {
     uint4 v[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; u++) {
@@ -380,7 +419,7 @@ __device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Se
       const uint4 now = v[0];                          // the rows move down: one copy of this code
 #pragma unroll
       for (int w = 0; w + 1 < kAhead; w++) v[w] = v[w + 1];
-      if (r - tid / kPerRow >= rp) break;              // no lane of the warp has a row
+      if (r - tid / kPerRow >= RP) break;              // no lane of the warp has a row
       const T* e = reinterpret_cast<const T*>(&now);
       float x[8], amax = 0.f;
 #pragma unroll
@@ -393,14 +432,14 @@ __device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Se
 #pragma unroll
       for (int o = kPerRow / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const float sc = row_scale(amax), inv = __uint_as_float((254u << 23) - __float_as_uint(sc));
-      if (r < rp) {
+      if (r < RP) {
         uint32_t c[2][TERMS];
 #pragma unroll
         for (int j = 0; j < 2; j++)
           split4<TERMS>(make_float2(x[4 * j] * inv, x[4 * j + 1] * inv), make_float2(x[4 * j + 2] * inv, x[4 * j + 3] * inv), c[j]);
 #pragma unroll
         for (int t = 0; t < TERMS; t++) {
-          const int n = t * rp + r;
+          const int n = t * RP + r;
           uint8_t* to = q_s + (c8 >> 7) * (N * 128) + n * 128 + ((((c8 & 127) >> 4) ^ (n & 7)) << 4) + (c8 & 8);
           *reinterpret_cast<uint2*>(to) = make_uint2(c[0][t], c[1][t]);
         }
@@ -410,27 +449,29 @@ __device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Se
   }
 }
 
-// RMAX: most query rows of a chunk.
-template <typename T, int HD, int RMAX>
-__global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
+// RP: query rows of a chunk, padded. It is known here so that the loops over the rows have no branches: with one, every
+// eight rows would wait for their own loads.
+template <typename T, int HD, int RP>
+__global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
     cache_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
   constexpr int TERMS = __is_same(T, __nv_bfloat16) ? 2 : 3;
   constexpr int PANELS = panels_of(HD), STAGE = stage_bytes(HD);
   constexpr int ROWB = HD < 128 ? HD : 128;            // bytes of a key in a panel
   constexpr int PANEL = kTile * 128;                   // bytes between panels (HD = 256)
-  constexpr int CH = RMAX / 8;                         // chunks of 8 rows
+  constexpr int CH = RP / 8;                           // chunks of 8 rows
+  constexpr int NS = score_columns(RP), N = weight_columns(TERMS, RP);
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  const int S = a.p.stages, N = a.p.n, NS = a.p.ns, rp = a.p.rp;
-  const int q_bytes = N * 128 * PANELS;
+  constexpr int q_bytes = N * 128 * PANELS;
+  const int S = a.p.stages;
   uint8_t* ring = sm;
   uint8_t* q_s = ring + (size_t)S * STAGE;             // two buffers, by turns for the segments
   uint8_t* p_s = q_s + 2 * q_bytes;
   RowState& rs = *reinterpret_cast<RowState*>(p_s + kPBytes);
   uint64_t* bars = reinterpret_cast<uint64_t*>(&rs + 1);
   uint64_t *full = bars, *empty = bars + kMaxStages, *s_full = bars + 2 * kMaxStages, *s_free = s_full + 2, *q_full = s_full + 4,
-           *q_free = s_full + 6, *p_full = s_full + 8, *p_free = s_full + 9, *drained = s_full + 10;
+           *q_free = s_full + 6, *p_full = s_full + 8, *p_free = s_full + 9, *drained = s_full + 10, *q_first = s_full + 11;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 12);
   // Set when a softmax wait gave up, by turns for the stretches between two points where all softmax threads look
   // (just behind a barrier), so that all of them see the same and leave together
@@ -448,12 +489,13 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
     for (int i = 0; i < 2; i++) {
       mbar_init(smem_u32(&s_full[i]), 2);              // the MMAs, and the warp that issued them
       mbar_init(smem_u32(&s_free[i]), 4);
-      mbar_init(smem_u32(&q_full[i]), 1);
+      mbar_init(smem_u32(&q_full[i]), 2);              // the two query warps
       mbar_init(smem_u32(&q_free[i]), 2);              // the MMAs, and the softmax warps
     }
     mbar_init(smem_u32(p_full), 4);
     mbar_init(smem_u32(p_free), 1);
     mbar_init(smem_u32(drained), 1);
+    mbar_init(smem_u32(q_first), kThreads / 32 - 1);
     dead[0] = dead[1] = 0;
     fence_barrier_init();
   }
@@ -473,6 +515,7 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
   {
     const int per = (a.n_req + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
     int mine = 0;
+#pragma unroll 1
     for (int j = 0; j < per; j++)
       if (b0 + j < a.n_req) {
         words[b0 + j] = read_request(a, b0 + j);
@@ -492,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
     int at = s - mine;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; w++) at += w < warp ? scan[w] : 0;
+#pragma unroll 1
     for (int j = 0; j < per; j++)
       if (b0 + j < a.n_req) {
         const int u = before[b0 + j];
@@ -520,13 +564,22 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
   const uint32_t tmem_o = tmem + 2 * NS;
   Segment sg;
 
-  constexpr bool kSplitRegs = RMAX == kRowsOfTwo;
+  constexpr bool kSplitRegs = RP > 8 && RP <= kRowsOfTwo;
+  // queries of the first segment: all warps but the copy warp, which starts on the keys
+  if (warp > 0) {
+    Walk w = walk;
+    if (w.next(a, before, words, sg)) prepare_queries<T, HD, TERMS, RP>(a, sg, q_s, rs.qs[0], threadIdx.x - 32, kThreads - 32);
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(q_first));
+  }
   if (warp < 4) {
   if (kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 0) {
     // ---- copies: one per block of the tile (and 128-byte panel), each by a lane of its own, which also leaves the
     // block's scales for the softmax -----------------------------------------------------------------------
-    int seq = 0, g = 0;
+    Ring at;
+    int g = 0;
     bool ok = true;
     const int nb = kTile >> a.log_t;
     while (ok && walk.next(a, before, words, sg)) {
@@ -534,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
       const int idx0 = (sg.r.s0 >> a.log_t) + lane;
       auto entry_of = [&](int t) {                     // this lane's block of tile t (as it is), -1: none
         const int idx = idx0 + t * nb;
-        return lane < nb && t < sg.t1 && ((long long)idx << a.log_t) < sg.r.len ? table[idx % a.table_blocks] : -1;
+        return lane < nb && t >= sg.t0 && t < sg.t1 && ((long long)idx << a.log_t) < sg.r.len ? table[idx % a.table_blocks] : -1;
       };
       struct Block {
         int e;
@@ -550,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
         return b;
       };
       auto copy = [&](const CUtensorMap* map, const Block& b, bool key) {
-        const int slot = seq % S;
-        if (seq >= S) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&empty[slot]), (seq / S + 1) & 1, a.err, kErrTimeoutCache));
+        const int slot = at.slot;
+        if (at.fill > 0) ok = wait_bar_warp(&empty[slot], at.fill + 1, a.err);
         if (!ok) return;
         // The softmax has read the constants that these replace: the ring of tiles is deeper than the copies run
         // ahead. This stage was free, so the scores of the tile S / 2 back were issued, and the two score
@@ -576,41 +629,46 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
           for (int p = 0; p < PANELS; p++) tma_load_5d(dst + p * PANEL, map, p * 128, 0, sg.head, b.e, a.layer, bar);
         }
         __syncwarp();
-        seq++;
+        at.next(S);
         if (key) g++;
       };
-      // entries two and three tiles ahead, scales one ahead
-      Block cur = block_of(entry_of(sg.t0)), nxt = block_of(entry_of(sg.t0 + 1));
-      int far = entry_of(sg.t0 + 2);
-      copy(&kmap, cur, true);
-      for (int t = sg.t0; ok && t < sg.t1; t++) {
+      // entries three tiles ahead, scales two ahead of the values: K of tile t + 1, then V of tile t
+      Block cur{-1, 0.f, 0.f}, nxt = cur;
+      int far = -1;
+#pragma unroll 1
+      for (int t = sg.t0 - 3; ok && t < sg.t1; t++) {
         const Block after = block_of(far);
         far = entry_of(t + 3);
-        if (t + 1 < sg.t1) copy(&kmap, nxt, true);
-        if (ok) copy(&vmap, cur, false);
+#pragma unroll 1
+        for (int side = 0; ok && side < 2; side++) {
+          if (side == 0 ? t + 1 < sg.t0 || t + 1 >= sg.t1 : t < sg.t0) continue;
+          copy(side == 0 ? &kmap : &vmap, side == 0 ? nxt : cur, side == 0);
+        }
         cur = nxt;
         nxt = after;
       }
     }
     // no copy may be in flight when the CTA leaves: the last fill of every stage has landed
-    for (int j = max(0, seq - S); j < seq; j++) mbar_wait_bounded(smem_u32(&full[j % S]), (j / S) & 1, nullptr, 0);
+    for (int i = 0; i < S; i++) {
+      const int fills = at.fill + (i < at.slot);
+      if (fills > 0) wait_bar(&full[i], fills - 1, nullptr);
+    }
   } else if (warp == 1) {
     // ---- MMAs ---------------------------------------------------------------------------------------------
     const uint32_t id_s = idesc_e4m3(NS, false), id_o = idesc_e4m3(N, true);
     const uint32_t ring_a = smem_u32(ring);
     const uint64_t qd0 = smem_desc(smem_u32(q_s), 16, 1024, 2), pd = smem_desc(smem_u32(p_s), 16, 1024, 2);
-    int base = 0, g = 0, n_seg = 0, pv_done = 0;       // g: tiles so far
+    Ring at;                                           // consumed in the order of the copies
+    int g = 0, n_seg = 0, pv_done = 0;                 // g: tiles so far
     bool ok = true;
-    auto wait = [&](uint64_t* bar, int parity) {
-      return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), (uint32_t)parity & 1, a.err, kErrTimeoutCache));
-    };
+    auto wait = [&](uint64_t* bar, int parity) { return wait_bar_warp(bar, parity, a.err); };
     while (ok && walk.next(a, before, words, sg)) {
       const int n = sg.t1 - sg.t0;
       const uint64_t qd = qd0 + (uint64_t)((n_seg & 1) * (q_bytes >> 4));
-      ok = wait(&q_full[n_seg & 1], n_seg >> 1);
+      ok = n_seg == 0 ? wait(q_first, 0) : wait(&q_full[n_seg & 1], (n_seg - 1) >> 1);
       auto scores = [&](int t) {                       // tile t of the segment
-        const int sq = base + (t == 0 ? 0 : 2 * t - 1), slot = sq % S, gg = g + t;
-        ok = ok && wait(&full[slot], sq / S);
+        const int slot = at.slot, gg = g + t;
+        ok = ok && wait(&full[slot], at.fill);
         if (ok && gg >= 2) ok = wait(&s_free[gg & 1], (gg >> 1) + 1);
         if (!ok) return;
         tc05_fence_after();
@@ -621,19 +679,21 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
           const uint64_t ka = kd + (uint64_t)((ks / 4) * (PANEL >> 4) + (ks % 4) * 2);
           const uint64_t qa = qd + (uint64_t)((ks / 4) * (N * 8) + (ks % 4) * 2);
 #pragma unroll
-          for (int i = 0; i < TERMS; i++) umma_e4m3_warp(d, ka, qa + (uint64_t)(i * rp * 8), id_s, ks > 0 || i > 0);
+          for (int i = 0; i < TERMS; i++) umma_e4m3_warp(d, ka, qa + (uint64_t)(i * RP * 8), id_s, ks > 0 || i > 0);
         }
         umma_commit_warp(smem_u32(&empty[slot]));
         umma_commit_warp(smem_u32(&s_full[gg & 1]));
         if (t + 1 == n) umma_commit_warp(smem_u32(&q_free[n_seg & 1]));
         if (lane == 0) mbar_arrive(smem_u32(&s_full[gg & 1]));   // passes the copy warp's constants on
         __syncwarp();
+        at.next(S);
       };
-      if (ok) scores(0);
-      for (int t = 0; ok && t < n; t++) {
+#pragma unroll 1
+      for (int t = -1; ok && t < n; t++) {
         if (t + 1 < n) scores(t + 1);
-        const int sq = base + (t + 1 < n ? 2 * t + 2 : 2 * n - 1), slot = sq % S, gg = g + t;
-        ok = ok && wait(&full[slot], sq / S) && wait(p_full, gg);
+        if (t < 0) continue;
+        const int slot = at.slot, gg = g + t;
+        ok = ok && wait(&full[slot], at.fill) && wait(p_full, gg);
         if (!ok) break;
         tc05_fence_after();
         const uint32_t va = ring_a + slot * STAGE;
@@ -647,26 +707,27 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
         umma_commit_warp(smem_u32(&empty[slot]));
         umma_commit_warp(smem_u32(p_free));
         pv_done = gg + 1;
+        at.next(S);
       }
-      base += 2 * n;
       g += n;
       n_seg++;
     }
     // nothing of this CTA may still run on the tensor core when its memory is freed. After a wait that gave up
     // there may be scores without a probability product: their commits have a barrier of their own
-    if (pv_done > 0) mbar_wait_bounded(smem_u32(p_free), (uint32_t)(pv_done - 1) & 1, a.err, kErrTimeoutCache);
+    if (pv_done > 0) wait_bar(p_free, pv_done - 1, a.err);
     if (!ok) {
       umma_commit_warp(smem_u32(drained));
-      mbar_wait_bounded(smem_u32(drained), 0, nullptr, 0);
+      wait_bar(drained, 0, nullptr);
     }
-  } else if (warp == 2) {
-    // ---- queries of the segments after the first, while the one before is at work ---------------------------
+  } else {
+    // ---- queries of the later segments, while the one before is at work ---------------------------------------
     bool ok = true;
+#pragma unroll 1
     for (int k = 0; ok && walk.next(a, before, words, sg); k++) {
       if (k == 0) continue;
-      if (k >= 2) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&q_free[k & 1]), ((k >> 1) + 1) & 1, a.err, kErrTimeoutCache));
+      if (k >= 2) ok = wait_bar_warp(&q_free[k & 1], (k >> 1) + 1, a.err);
       if (!ok) break;
-      prepare_queries<T, HD, TERMS>(a, sg, q_s + (k & 1) * q_bytes, rs.qs[k & 1], lane, 32);
+      prepare_queries<T, HD, TERMS, RP>(a, sg, q_s + (k & 1) * q_bytes, rs.qs[k & 1], threadIdx.x - 64, 64);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&q_full[k & 1]));
@@ -681,12 +742,12 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
     int base = 0, g = 0, look = 0, n_seg = 0;
     bool gone = false;
     auto wait = [&](uint64_t* bar, int parity) {
-      if (!mbar_wait_bounded(smem_u32(bar), (uint32_t)parity & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
+      if (!wait_bar(bar, parity, a.err)) dead[look & 1] = 1;
       __syncwarp();
     };
     while (!gone && walk.next(a, before, words, sg)) {
       const int n_tiles = sg.t1 - sg.t0, r0 = sg.chunk * a.p.rc, rows = min(a.p.rc, sg.r.n * a.grp - r0);
-      if (key < rp) {
+      if (key < RP) {
         rs.neg_m[key] = 0.f;
         rs.unset[key] = key < rows;
         int lo = 0, hi = 0;
@@ -699,16 +760,8 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
         rs.hi[key] = hi;
       }
       const float* row_qs = rs.qs[n_seg & 1];
-      if (n_seg == 0) {
-        prepare_queries<T, HD, TERMS>(a, sg, q_s, rs.qs[0], threadIdx.x - kSoftmax0, 128);
-        fence_proxy_async();
-      } else {
-        wait(&q_full[n_seg & 1], n_seg >> 1);
-      }
-      __syncwarp();
+      wait(n_seg == 0 ? q_first : &q_full[n_seg & 1], n_seg == 0 ? 0 : (n_seg - 1) >> 1);   // the query scales
       softmax_sync();
-      if (n_seg == 0 && threadIdx.x == kSoftmax0) mbar_arrive(smem_u32(&q_full[0]));
-      __syncwarp();
 
       int lo_all, hi_all, dummy;                       // keys that every row sees
       row_range(a, sg.r, r0 / a.grp, dummy, hi_all);
@@ -728,109 +781,23 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
         const float2 ka = make_float2(kc.x, kc.x), vb2 = make_float2(kc.y, kc.y), inv2 = make_float2(kc.z, kc.z);
         const bool seen = kc.w != 0.f && pos >= sg.r.lo && pos < sg.r.len;   // by some row
         const bool whole = seen && pos >= lo_all && pos < hi_all;             // by every row
-        // x = t - m of this key for each row
-        float2 x[CH * 4];
-        float top = -INFINITY;
-        const uint32_t ts = tmem + lanes + (uint32_t)((gg & 1) * NS);
-        uint32_t s8[2][8];
-        tmem_start8(ts, s8[0]);
-#pragma unroll
-        for (int ch = 0; ch < CH; ch++) {
-          if (ch * 8 < rp) {
-            const float4* qp = reinterpret_cast<const float4*>(row_qs + ch * 8);
-            const float4* mp = reinterpret_cast<const float4*>(&rs.neg_m[ch * 8]);
-            const float4 q0 = qp[0], q1 = qp[1], m0 = mp[0], m1 = mp[1];
-            tmem_wait8(s8[ch & 1]);
-            if ((ch + 1) * 8 < rp) tmem_start8(ts + ch * 8 + 8, s8[(ch + 1) & 1]);
-            const float2 q2[4] = {{q0.x, q0.y}, {q0.z, q0.w}, {q1.x, q1.y}, {q1.z, q1.w}};
-            const float2 m2[4] = {{m0.x, m0.y}, {m0.z, m0.w}, {m1.x, m1.y}, {m1.z, m1.w}};
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-              const float2 sc = make_float2(__uint_as_float(s8[ch & 1][2 * j]), __uint_as_float(s8[ch & 1][2 * j + 1]));
-              const float2 v = fma2(mul2(sc, q2[j]), ka, add2(vb2, m2[j]));
-              x[ch * 4 + j] = v;
-              top = fmaxf(top, fmaxf(v.x, v.y));
-            }
-          }
-        }
-        tc05_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s_free[gg & 1]));
-        if (__any_sync(0xffffffffu, !whole)) {
-          // keys that no row sees, or some rows and others not (ends, causal and window edges)
-          top = -INFINITY;
-#pragma unroll
-          for (int r = 0; r < CH * 4; r++)
-            if (r * 2 < rp) {
-              const int2 lo = *reinterpret_cast<const int2*>(&rs.lo[2 * r]), hi = *reinterpret_cast<const int2*>(&rs.hi[2 * r]);
-              if (!(seen && (whole || (pos >= lo.x && pos < hi.x)))) x[r].x = -INFINITY;
-              if (!(seen && (whole || (pos >= lo.y && pos < hi.y)))) x[r].y = -INFINITY;
-              top = fmaxf(top, fmaxf(x[r].x, x[r].y));
-            }
-        }
-        const bool move = softmax_any(top > kMax || unset_any);
-        gone = dead[look++ & 1];
-        if (gone) break;
-        if (move) {
-          // new references: a row's largest t over the tile at 2^kTop, where it passed 2^kMax or is the first
-#pragma unroll
-          for (int ch = 0; ch < CH; ch++) {
-            if (ch * 8 < rp) {
-              float v8[8];
-#pragma unroll
-              for (int j = 0; j < 4; j++) v8[2 * j] = x[ch * 4 + j].x, v8[2 * j + 1] = x[ch * 4 + j].y;
-              const float mx = reduce8(v8, [](float p, float q) { return fmaxf(p, q); });
-              if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = mx;
-            }
-          }
-          softmax_sync();
-          bool still = false;
-          if (key < rp) {
-            const float mx = fmaxf(fmaxf(rs.red[0][key], rs.red[1][key]), fmaxf(rs.red[2][key], rs.red[3][key]));
-            const bool first = rs.unset[key] && mx > -INFINITY;
-            const float by = first || mx > kMax ? mx - kTop : 0.f;        // the reference grows by this
-            rs.red[0][key] = by;
-            rs.f[key] = first ? 0.f : ex2(-by);
-            rs.neg_m[key] -= by;
-            if (first) rs.unset[key] = 0;
-            still = rs.unset[key];
-          }
-          unset_any = softmax_any(still);
-#pragma unroll
-          for (int r = 0; r < CH * 4; r++)
-            if (r * 2 < rp) {
-              const float2 by = *reinterpret_cast<const float2*>(&rs.red[0][2 * r]), f = *reinterpret_cast<const float2*>(&rs.f[2 * r]);
-              x[r] = make_float2(x[r].x - by.x, x[r].y - by.y);
-              l[r] = mul2(l[r], f);
-            }
-          if (t > 0) {
-            wait(p_free, gg - 1);
-            tc05_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < PANELS * TERMS; c++) {
-              const uint32_t to = tmem_o + lanes + (uint32_t)((c / TERMS) * N + (c % TERMS) * rp);
-#pragma unroll 1
-              for (int ch = 0; ch < rp; ch += 8) {
-                float o8[8];
-                tmem_ld8(to + ch, o8);
-#pragma unroll
-                for (int j = 0; j < 8; j++) o8[j] *= rs.f[ch + j];
-                tmem_st8(to + ch, o8);
-              }
-            }
-            tmem_wait_st();
-          }
-          softmax_sync();                              // red has been read
-        }
-        // the probabilities of the tile before have been read
-        if (gg > 0) wait(p_free, gg - 1);
+        // Edges: which rows see this key. A key that no row sees must not reach the product: its code bytes may be
+        // anything, and 0 * NaN is NaN. Nor may a NaN value reach the rows that do not see its key: there it becomes
+        // 0 and the weight becomes NaN for the rows that do.
+        const bool edge = __any_sync(0xffffffffu, !whole);
+        uint32_t sees[2] = {~0u, ~0u};                   // rows 0-31, 32-63
+        bool v_nan = false;
         if (!whole) {
-          // A key that no row sees must not reach the product: its code bytes may be anything, and 0 * NaN
-          // is NaN. Nor may a NaN value reach the rows that do not see its key: there it becomes 0 and the
-          // weight becomes NaN for the rows that do.
-          bool v_nan = false;
+          sees[0] = sees[1] = 0;
+          if (seen)
+#pragma unroll 1
+            for (int r = 0; r < RP; r++) {
+              const uint32_t bit = (uint32_t)(pos >= rs.lo[r] && pos < rs.hi[r]) << (r & 31);
+              if (r < 32) sees[0] |= bit;
+              else sees[1] |= bit;
+            }
           const int sq = base + (t + 1 < n_tiles ? 2 * t + 2 : 2 * n_tiles - 1), slot = sq % S;
-          if (!mbar_wait_bounded(smem_u32(&full[slot]), (sq / S) & 1, a.err, kErrTimeoutCache)) dead[look & 1] = 1;
+          if (!wait_bar(&full[slot], sq / S, a.err)) dead[look & 1] = 1;
 #pragma unroll 1
           for (int c = 0; c < HD / 16; c++) {
             uint4* at = reinterpret_cast<uint4*>(ring + (size_t)slot * STAGE + (c >> 3) * PANEL + key * ROWB + (c & 7) * 16);
@@ -844,33 +811,151 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
             }
             *at = make_uint4(w.x & ~bad.x, w.y & ~bad.y, w.z & ~bad.z, w.w & ~bad.w);
           }
-          if (v_nan) {
-#pragma unroll
-            for (int r = 0; r < CH * 4; r++)
-              if (r * 2 < rp) {
-                if (x[r].x != -INFINITY) x[r].x = __int_as_float(0x7fffffff);
-                if (x[r].y != -INFINITY) x[r].y = __int_as_float(0x7fffffff);
-              }
-          }
         }
+        __syncwarp();
+        // x = t - m of this key for each row; once more when references have moved (no x passes kMax then)
+        float2 x[CH * 4];
+        const uint32_t ts = tmem + lanes + (uint32_t)((gg & 1) * NS);
+#pragma unroll 1
+        for (int pass = 0; pass < 2; pass++) {
+          uint32_t s8[CH][8], high = 0;                // high: chunks with a value above kMax
+#pragma unroll
+          for (int ch = 0; ch < CH; ch++)
+            tmem_start8(ts + ch * 8, s8[ch]);
+#pragma unroll
+          for (int ch = 0; ch < CH; ch++) tmem_wait8(s8[ch]);
+#pragma unroll
+          for (int ch = 0; ch < CH; ch++) {
+            {
+              const float4* qp = reinterpret_cast<const float4*>(row_qs + ch * 8);
+              const float4* mp = reinterpret_cast<const float4*>(&rs.neg_m[ch * 8]);
+              const float4 q0 = qp[0], q1 = qp[1], m0 = mp[0], m1 = mp[1];
+              const float2 q2[4] = {{q0.x, q0.y}, {q0.z, q0.w}, {q1.x, q1.y}, {q1.z, q1.w}};
+              const float2 m2[4] = {{m0.x, m0.y}, {m0.z, m0.w}, {m1.x, m1.y}, {m1.z, m1.w}};
+              float top = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < 4; j++) {
+                const float2 sc = make_float2(__uint_as_float(s8[ch][2 * j]), __uint_as_float(s8[ch][2 * j + 1]));
+                const float2 v = fma2(mul2(sc, q2[j]), ka, add2(vb2, m2[j]));
+                x[ch * 4 + j] = v;
+                top = fmaxf(top, fmaxf(v.x, v.y));
+              }
+              if (top > kMax) high |= 1u << ch;
+            }
+          }
+          if (edge) {
+            high = 0;
+            const float nan = __int_as_float(0x7fffffff);
+#pragma unroll
+            for (int r = 0; r < CH * 4; r++) {
+              const uint32_t two = sees[r / 16] >> (2 * r % 32);
+              if (v_nan) x[r] = make_float2(nan, nan);
+              if (!(two & 1)) x[r].x = -INFINITY;
+              if (!(two & 2)) x[r].y = -INFINITY;
+              if (fmaxf(x[r].x, x[r].y) > kMax) high |= 1u << (r / 4);
+            }
+          }
+          if (pass == 1) break;
+          // the probabilities of the tile before have been read, and its part of O is there
+          if (gg > 0) wait(p_free, gg - 1);
+          const bool move = softmax_any(high != 0 || unset_any);
+          gone = dead[look++ & 1];
+          if (gone || !move) break;
+          // New references: the chunks of rows where some row passed 2^kMax, or all while a row has seen no key, get
+          // each row's largest t over the tile.
+          high = __reduce_or_sync(0xffffffffu, high);
+          if (lane == 0) rs.high[quarter] = high;
+          softmax_sync();
+          high = unset_any ? (1u << (RP / 8)) - 1 : rs.high[0] | rs.high[1] | rs.high[2] | rs.high[3];
+#pragma unroll
+          for (int ch = 0; ch < CH; ch++) tmem_start8(ts + ch * 8, s8[ch]);
+#pragma unroll
+          for (int ch = 0; ch < CH; ch++) tmem_wait8(s8[ch]);
+#pragma unroll
+          for (int ch = 0; ch < CH; ch++) {
+            float v8[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+              const int r = ch * 8 + j;
+              const float tv = fmaf(__uint_as_float(s8[ch][j]) * row_qs[r], kc.x, kc.y);
+              v8[j] = (sees[r / 32] >> (r % 32)) & 1 ? tv : -INFINITY;
+            }
+            const float mx = reduce8(v8, [](float p, float q) { return fmaxf(p, q); });
+            if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = mx;
+          }
+          softmax_sync();
+          bool still = false;
+          if (key < RP) {
+            float by = 0.f;                            // the reference grows by this
+            bool first = false;
+            if ((high >> (key >> 3)) & 1) {
+              const float mx = fmaxf(fmaxf(rs.red[0][key], rs.red[1][key]), fmaxf(rs.red[2][key], rs.red[3][key])) + rs.neg_m[key];
+              first = rs.unset[key] && mx > -INFINITY;
+              if (first || mx > kMax) by = mx - kTop;
+            }
+            rs.f[key] = first ? 0.f : ex2(-by);
+            rs.neg_m[key] -= by;
+            if (first) rs.unset[key] = 0;
+            still = rs.unset[key];
+          }
+          unset_any = softmax_any(still);
+#pragma unroll
+          for (int r = 0; r < CH * 4; r++)
+            l[r] = mul2(l[r], *reinterpret_cast<const float2*>(&rs.f[2 * r]));
+          if (t > 0) {
+            tc05_fence_after();
+#pragma unroll 1
+            for (uint32_t left = high; left; left &= left - 1) {
+              const int r0 = 8 * (__ffs(left) - 1);
+#pragma unroll 1
+              for (int p = 0; p < PANELS; p++) {
+                const uint32_t to = tmem_o + lanes + (uint32_t)(p * N + r0 * TERMS);
+                uint32_t o8[TERMS][8];
+#pragma unroll
+                for (int i = 0; i < TERMS; i++) tmem_start8(to + i * 8, o8[i]);
+#pragma unroll
+                for (int i = 0; i < TERMS; i++) {
+                  tmem_wait8(o8[i]);
+                  float o[8];
+#pragma unroll
+                  for (int j = 0; j < 8; j++) o[j] = __uint_as_float(o8[i][j]) * rs.f[r0 + j];
+                  tmem_st8(to + i * 8, o);
+                }
+              }
+            }
+            tmem_wait_st();
+          }
+          softmax_sync();                              // f and high have been read
+        }
+        if (gone) break;
+        tc05_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s_free[gg & 1]));
         __syncwarp();
 #pragma unroll
         for (int ch = 0; ch < CH; ch++) {
-          if (ch * 8 < rp) {
+          {
             float2 w[4];
 #pragma unroll
             for (int j = 0; j < 4; j++) {
               w[j] = make_float2(ex2(x[ch * 4 + j].x), ex2(x[ch * 4 + j].y));
               l[ch * 4 + j] = fma2(w[j], inv2, l[ch * 4 + j]);
             }
-            uint32_t c[2][TERMS];
-            split4<TERMS>(w[0], w[1], c[0]);
-            split4<TERMS>(w[2], w[3], c[1]);
+            // columns of the product: per chunk of rows, its terms side by side (with two terms one 16-byte piece)
+            uint2 c[TERMS];
+            split8<TERMS>(w, c);
+            if constexpr (TERMS == 2) {
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + (uint32_t)((ch ^ (key & 7)) << 4)), "r"(c[0].x),
+                           "r"(c[0].y), "r"(c[1].x), "r"(c[1].y)
+                           : "memory");
+            } else {
 #pragma unroll
-            for (int i = 0; i < TERMS; i++) {
-              const int o = i * rp + ch * 8;
-              const uint32_t to = p_row + ((((uint32_t)o >> 4) ^ (key & 7)) << 4) + (o & 8);
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(c[0][i]), "r"(c[1][i]) : "memory");
+              for (int i = 0; i < TERMS; i++) {
+                const int o = (ch * TERMS + i) * 8;
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(p_row + (uint32_t)((((o >> 4) ^ (key & 7)) << 4) + (o & 8))),
+                             "r"(c[i].x), "r"(c[i].y)
+                             : "memory");
+              }
             }
           }
         }
@@ -885,15 +970,12 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
 
       // ---- end of the segment: L over the keys, then O -------------------------------------------------------
 #pragma unroll
-      for (int ch = 0; ch < CH; ch++) {
-        if (ch * 8 < rp) {
-          float v8[8];
-#pragma unroll
-          for (int j = 0; j < 4; j++) v8[2 * j] = l[ch * 4 + j].x, v8[2 * j + 1] = l[ch * 4 + j].y;
+      for (int ch = 0; ch < CH; ch++)
+        {
+          const float v8[8] = {l[4 * ch].x, l[4 * ch].y, l[4 * ch + 1].x, l[4 * ch + 1].y, l[4 * ch + 2].x, l[4 * ch + 2].y, l[4 * ch + 3].x, l[4 * ch + 3].y};
           const float sum = reduce8(v8, [](float p, float q) { return p + q; });
           if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = sum;
         }
-      }
       wait(p_free, g - 1);
       softmax_sync();
       gone = dead[look++ & 1];
@@ -901,21 +983,29 @@ __global__ void __launch_bounds__(kThreads, RMAX <= kRowsOfTwo ? 2 : 1)
       if (threadIdx.x == kSoftmax0) mbar_arrive(smem_u32(&q_free[n_seg & 1]));
       const bool direct = sg.t0 == 0 && sg.t1 == sg.r.tiles && !a.k_own;
       const size_t slot = (size_t)blockIdx.x + sg.pair;
-      if (key < rp) {
+      if (key < RP) {
         const float L = (rs.red[0][key] + rs.red[1][key]) + (rs.red[2][key] + rs.red[3][key]);
         rs.f[key] = L == 0.f ? 0.f : 1.f / L;
-        if (!direct) a.part_ml[slot * rp + key] = make_float2(rs.unset[key] ? kUnset : -rs.neg_m[key], L);
+        if (!direct) a.part_ml[slot * RP + key] = make_float2(rs.unset[key] ? kUnset : -rs.neg_m[key], L);
       }
       softmax_sync();
       tc05_fence_after();
-      float* part = a.part_o + slot * rp * HD + key;
+      float* part = a.part_o + slot * RP * HD + key;
       T* out = static_cast<T*>(a.out) + key;
 #pragma unroll 1
       for (int p = 0; p < PANELS; p++) {
 #pragma unroll 1
         for (int ch = 0; ch < rows; ch += 8) {
+          uint32_t part8[TERMS][8];
           float o8[8];
-          tmem_sum8<TERMS>(tmem_o + lanes + (uint32_t)(p * N + ch), rp, o8);
+#pragma unroll
+          for (int i = 0; i < TERMS; i++) tmem_start8(tmem_o + lanes + (uint32_t)(p * N + ch * TERMS + i * 8), part8[i]);
+#pragma unroll
+          for (int i = 0; i < TERMS; i++) {
+            tmem_wait8(part8[i]);
+#pragma unroll
+            for (int j = 0; j < 8; j++) o8[j] = i == 0 ? __uint_as_float(part8[i][j]) : o8[j] + __uint_as_float(part8[i][j]);
+          }
           if (key < HD) {
 #pragma unroll
             for (int j = 0; j < 8; j++) {
@@ -1032,19 +1122,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
   for (int c = 0; c < PER; c++) row_store(out + c, o[c] * inv);
 }
 
-template <typename T, int HD, int RMAX>
+template <typename T, int HD, int RP>
 cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
   static std::atomic<int> smem_set[kMaxDevices];
-  cudaError_t e = ensure_smem_limit(cache_attn_kernel<T, HD, RMAX>, a.p.smem, smem_set);
+  cudaError_t e = ensure_smem_limit(cache_attn_kernel<T, HD, RP>, a.p.smem, smem_set);
   if (e != cudaSuccess) return e;
-  if (RMAX == kRowsOfTwo) {   // the softmax warps would wait for registers that the CTA does not have
+  if (RP > 8 && RP <= kRowsOfTwo) {   // the softmax warps would wait for registers that the CTA does not have
     static const int regs = [] {
       cudaFuncAttributes at{};
-      return cudaFuncGetAttributes(&at, cache_attn_kernel<T, HD, RMAX>) == cudaSuccess ? at.numRegs : 0;
+      return cudaFuncGetAttributes(&at, cache_attn_kernel<T, HD, RP>) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs < kStartRegs) return cudaErrorInvalidConfiguration;
   }
-  e = launch_pdl(cache_attn_kernel<T, HD, RMAX>, dim3(a.grid), dim3(kThreads), a.p.smem, s, a, kmap, vmap);
+  e = launch_pdl(cache_attn_kernel<T, HD, RP>, dim3(a.grid), dim3(kThreads), a.p.smem, s, a, kmap, vmap);
   if (e != cudaSuccess) return e;
   const long long tasks = (long long)a.n_req * a.n_kv * a.p.chunks * a.p.rc;
   return launch_pdl(cache_attn_join_kernel<T, HD>, dim3((unsigned)((tasks + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, s, a);
@@ -1052,9 +1142,14 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtens
 
 template <typename T, int HD>
 cudaError_t launch_rows(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
-  if (a.p.rp <= 8) return launch<T, HD, 8>(a, kmap, vmap, s);
-  if (a.p.rp <= kRowsOfTwo) return launch<T, HD, kRowsOfTwo>(a, kmap, vmap, s);
-  if constexpr (__is_same(T, __nv_bfloat16)) return launch<T, HD, 64>(a, kmap, vmap, s);
+  switch (a.p.rp) {
+    case 8: return launch<T, HD, 8>(a, kmap, vmap, s);
+    case 16: return launch<T, HD, 16>(a, kmap, vmap, s);
+    case 24: return launch<T, HD, 24>(a, kmap, vmap, s);
+    case 40: return launch<T, HD, 40>(a, kmap, vmap, s);
+    case 64:
+      if constexpr (__is_same(T, __nv_bfloat16)) return launch<T, HD, 64>(a, kmap, vmap, s);
+  }
   return cudaErrorInvalidValue;
 }
 
@@ -1077,9 +1172,9 @@ CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req) 
   const int limit = dtype == DFLASH_BF16 ? 64 : 40, rows = grp * max_q;
   p.chunks = (rows + limit - 1) / limit;
   p.rc = (rows + p.chunks - 1) / p.chunks;
-  p.rp = (p.rc + 7) / 8 * 8;
-  p.n = (p.terms * p.rp + 15) / 16 * 16;
-  p.ns = (p.rp + 15) / 16 * 16;
+  p.rp = p.rc <= 8 ? 8 : p.rc <= 16 ? 16 : p.rc <= 24 ? 24 : p.rc <= 40 ? 40 : 64;   // the kernels there are
+  p.n = weight_columns(p.terms, p.rp);
+  p.ns = score_columns(p.rp);
   const int cols = 2 * p.ns + panels_of(hd) * p.n;
   p.tmem_cols = 32;
   while (p.tmem_cols < cols) p.tmem_cols *= 2;
