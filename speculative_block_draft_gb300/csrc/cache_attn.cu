@@ -374,7 +374,7 @@ struct alignas(16) RowState {            // per query row of the CTA's chunk
   float4 key[kConstRing][kTile / 16];    // per tile and block: k_scale * scale * log2(e), log2(v_scale), 1 / v_scale, there or not
   float neg_m[kRowArrays];               // minus the reference
   float qs[2][kRowArrays];               // the row's query scale; by turns for the segments, as the queries
-  float f[kRowArrays];                   // factor of a moved reference; 1 / L at the end
+  float f[kRowArrays], by[kRowArrays];   // factor of a moved reference, minus its step; 1 / L at the end
   float red[4][kRowArrays];              // per softmax warp: maxima, sums
   uint32_t high[4];                      // per softmax warp: chunks of rows with a value above kMax
   int lo[kRowArrays], hi[kRowArrays];    // visible positions
@@ -394,15 +394,16 @@ __host__ __device__ inline size_t attn_fixed_smem(int hd, int n, int n_req) {
 
 // ---- the first kernel ----------------------------------------------------------------------------------
 // The queries of a segment as e4m3 terms in shared memory (rows of 128 bytes, swizzled as the MMA reads them; a
-// second panel for the columns from 128), by `threads` threads. A row is scaled so that its largest value lies
-// in (224, 448]; qs gets the scale.
+// second panel for the columns from 128), by `threads` >= 64 threads. A row is scaled so that its largest value
+// lies in (224, 448]; qs gets the scale.
 template <typename T, int HD, int TERMS, int RP>
 __device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Segment& sg, uint8_t* q_s, float* qs, int tid, int threads) {
   constexpr int kPerRow = HD / 8, kAhead = 5;          // lanes of a row; rows in flight per lane
   constexpr int N = weight_columns(TERMS, RP);
   const int r0 = sg.chunk * a.p.rc, rows = min(a.p.rc, sg.r.n * a.grp - r0);
   const int c8 = (tid % kPerRow) * 8, at_once = threads / kPerRow;
-  for (int first = tid / kPerRow; first < RP; first += kAhead * at_once) {
+  if (tid < RP && tid >= rows) qs[tid] = 0.f;          // padding: whatever is there counts nothing
+  for (int first = tid / kPerRow; first - tid / kPerRow < rows; first += kAhead * at_once) {
     uint4 v[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; u++) {
@@ -419,7 +420,7 @@ __device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Se
       const uint4 now = v[0];                          // the rows move down: one copy of this code
 #pragma unroll
       for (int w = 0; w + 1 < kAhead; w++) v[w] = v[w + 1];
-      if (r - tid / kPerRow >= RP) break;              // no lane of the warp has a row
+      if (r - tid / kPerRow >= rows) break;            // for the whole warp, and no lane has a row
       const T* e = reinterpret_cast<const T*>(&now);
       float x[8], amax = 0.f;
 #pragma unroll
@@ -432,7 +433,7 @@ __device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Se
 #pragma unroll
       for (int o = kPerRow / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const float sc = row_scale(amax), inv = __uint_as_float((254u << 23) - __float_as_uint(sc));
-      if (r < RP) {
+      if (r < rows) {
         uint32_t c[2][TERMS];
 #pragma unroll
         for (int j = 0; j < 2; j++)
@@ -606,9 +607,17 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
         const int slot = at.slot;
         if (at.fill > 0) ok = wait_bar_warp(&empty[slot], at.fill + 1, a.err);
         if (!ok) return;
-        // The softmax has read the constants that these replace: the ring of tiles is deeper than the copies run
-        // ahead. This stage was free, so the scores of the tile S / 2 back were issued, and the two score
-        // buffers let that happen when those of two tiles before it had been read, its constants with them.
+        const uint32_t bar = smem_u32(&full[slot]);
+        const int n = __popc(__ballot_sync(0xffffffffu, b.e >= 0));
+        if (b.e >= 0) {
+          const uint32_t dst = smem_u32(ring + (size_t)slot * STAGE) + ((uint32_t)(lane * ROWB) << a.log_t);
+#pragma unroll
+          for (int p = 0; p < PANELS; p++) tma_load_5d(dst + p * PANEL, map, p * 128, 0, sg.head, b.e, a.layer, bar);
+        }
+        // The constants, behind the copies: their loads may still be under way. The softmax has read those that they
+        // replace: the ring of tiles is deeper than the copies run ahead. This stage was free, so the scores of the
+        // tile S / 2 back were issued, and the two score buffers let that happen when those of two tiles before it
+        // had been read, its constants with them.
         if (key && lane < nb) {
           float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
           if (b.e >= 0) {
@@ -618,16 +627,9 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
           }
           rs.key[g % kConstRing][lane] = c;
         }
-        const uint32_t bar = smem_u32(&full[slot]);
-        const int n = __popc(__ballot_sync(0xffffffffu, b.e >= 0));
         __syncwarp();
+        // the only arrival of the fill, so none of its bytes can end it before
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * ((uint32_t)HD << a.log_t));
-        __syncwarp();
-        if (b.e >= 0) {
-          const uint32_t dst = smem_u32(ring + (size_t)slot * STAGE) + ((uint32_t)(lane * ROWB) << a.log_t);
-#pragma unroll
-          for (int p = 0; p < PANELS; p++) tma_load_5d(dst + p * PANEL, map, p * 128, 0, sg.head, b.e, a.layer, bar);
-        }
         __syncwarp();
         at.next(S);
         if (key) g++;
@@ -813,95 +815,91 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
           }
         }
         __syncwarp();
-        // x = t - m of this key for each row; once more when references have moved (no x passes kMax then)
+        // x = t - m of this key for each row
         float2 x[CH * 4];
+        uint32_t high = 0;                               // chunks of rows with an x above kMax
         const uint32_t ts = tmem + lanes + (uint32_t)((gg & 1) * NS);
-#pragma unroll 1
-        for (int pass = 0; pass < 2; pass++) {
-          uint32_t s8[CH][8], high = 0;                // high: chunks with a value above kMax
-#pragma unroll
-          for (int ch = 0; ch < CH; ch++)
-            tmem_start8(ts + ch * 8, s8[ch]);
-#pragma unroll
-          for (int ch = 0; ch < CH; ch++) tmem_wait8(s8[ch]);
-#pragma unroll
-          for (int ch = 0; ch < CH; ch++) {
-            {
-              const float4* qp = reinterpret_cast<const float4*>(row_qs + ch * 8);
-              const float4* mp = reinterpret_cast<const float4*>(&rs.neg_m[ch * 8]);
-              const float4 q0 = qp[0], q1 = qp[1], m0 = mp[0], m1 = mp[1];
-              const float2 q2[4] = {{q0.x, q0.y}, {q0.z, q0.w}, {q1.x, q1.y}, {q1.z, q1.w}};
-              const float2 m2[4] = {{m0.x, m0.y}, {m0.z, m0.w}, {m1.x, m1.y}, {m1.z, m1.w}};
-              float top = -INFINITY;
-#pragma unroll
-              for (int j = 0; j < 4; j++) {
-                const float2 sc = make_float2(__uint_as_float(s8[ch][2 * j]), __uint_as_float(s8[ch][2 * j + 1]));
-                const float2 v = fma2(mul2(sc, q2[j]), ka, add2(vb2, m2[j]));
-                x[ch * 4 + j] = v;
-                top = fmaxf(top, fmaxf(v.x, v.y));
-              }
-              if (top > kMax) high |= 1u << ch;
-            }
-          }
-          if (edge) {
-            high = 0;
-            const float nan = __int_as_float(0x7fffffff);
-#pragma unroll
-            for (int r = 0; r < CH * 4; r++) {
-              const uint32_t two = sees[r / 16] >> (2 * r % 32);
-              if (v_nan) x[r] = make_float2(nan, nan);
-              if (!(two & 1)) x[r].x = -INFINITY;
-              if (!(two & 2)) x[r].y = -INFINITY;
-              if (fmaxf(x[r].x, x[r].y) > kMax) high |= 1u << (r / 4);
-            }
-          }
-          if (pass == 1) break;
-          // the probabilities of the tile before have been read, and its part of O is there
-          if (gg > 0) wait(p_free, gg - 1);
-          const bool move = softmax_any(high != 0 || unset_any);
-          gone = dead[look++ & 1];
-          if (gone || !move) break;
-          // New references: the chunks of rows where some row passed 2^kMax, or all while a row has seen no key, get
-          // each row's largest t over the tile.
-          high = __reduce_or_sync(0xffffffffu, high);
-          if (lane == 0) rs.high[quarter] = high;
-          softmax_sync();
-          high = unset_any ? (1u << (RP / 8)) - 1 : rs.high[0] | rs.high[1] | rs.high[2] | rs.high[3];
+        {
+          uint32_t s8[CH][8];
 #pragma unroll
           for (int ch = 0; ch < CH; ch++) tmem_start8(ts + ch * 8, s8[ch]);
 #pragma unroll
           for (int ch = 0; ch < CH; ch++) tmem_wait8(s8[ch]);
+          tc05_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s_free[gg & 1]));
 #pragma unroll
           for (int ch = 0; ch < CH; ch++) {
-            float v8[8];
+            const float4* qp = reinterpret_cast<const float4*>(row_qs + ch * 8);
+            const float4* mp = reinterpret_cast<const float4*>(&rs.neg_m[ch * 8]);
+            const float4 q0 = qp[0], q1 = qp[1], m0 = mp[0], m1 = mp[1];
+            const float2 q2[4] = {{q0.x, q0.y}, {q0.z, q0.w}, {q1.x, q1.y}, {q1.z, q1.w}};
+            const float2 m2[4] = {{m0.x, m0.y}, {m0.z, m0.w}, {m1.x, m1.y}, {m1.z, m1.w}};
+            float top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-              const int r = ch * 8 + j;
-              const float tv = fmaf(__uint_as_float(s8[ch][j]) * row_qs[r], kc.x, kc.y);
-              v8[j] = (sees[r / 32] >> (r % 32)) & 1 ? tv : -INFINITY;
+            for (int j = 0; j < 4; j++) {
+              const float2 sc = make_float2(__uint_as_float(s8[ch][2 * j]), __uint_as_float(s8[ch][2 * j + 1]));
+              const float2 v = fma2(mul2(sc, q2[j]), ka, add2(vb2, m2[j]));
+              x[ch * 4 + j] = v;
+              top = fmaxf(top, fmaxf(v.x, v.y));
             }
-            const float mx = reduce8(v8, [](float p, float q) { return fmaxf(p, q); });
-            if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = mx;
+            if (top > kMax) high |= 1u << ch;
+          }
+        }
+        if (edge) {
+          high = 0;
+          const float nan = __int_as_float(0x7fffffff);
+#pragma unroll
+          for (int r = 0; r < CH * 4; r++) {
+            const uint32_t two = sees[r / 16] >> (2 * r % 32);
+            if (v_nan) x[r] = make_float2(nan, nan);
+            if (!(two & 1)) x[r].x = -INFINITY;
+            if (!(two & 2)) x[r].y = -INFINITY;
+            if (fmaxf(x[r].x, x[r].y) > kMax) high |= 1u << (r / 4);
+          }
+        }
+        // the probabilities of the tile before have been read, and its part of O is there
+        if (gg > 0) wait(p_free, gg - 1);
+        const bool move = softmax_any(high != 0 || unset_any);
+        gone = dead[look++ & 1];
+        if (gone) break;
+        if (move) {
+          // New references: in the chunks of rows where some row passed 2^kMax, or all while a row has seen no key, the
+          // largest x of a row over the tile goes to kTop where it passed kMax or is the row's first.
+          high = __reduce_or_sync(0xffffffffu, high);
+          if (lane == 0) rs.high[quarter] = high;
+          softmax_sync();
+          high = unset_any ? (1u << CH) - 1 : rs.high[0] | rs.high[1] | rs.high[2] | rs.high[3];
+#pragma unroll
+          for (int ch = 0; ch < CH; ch++) {
+            if ((high >> ch) & 1) {
+              const float v8[8] = {x[4 * ch].x, x[4 * ch].y, x[4 * ch + 1].x, x[4 * ch + 1].y, x[4 * ch + 2].x, x[4 * ch + 2].y, x[4 * ch + 3].x, x[4 * ch + 3].y};
+              const float mx = reduce8(v8, [](float p, float q) { return fmaxf(p, q); });
+              if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = mx;
+            }
           }
           softmax_sync();
           bool still = false;
           if (key < RP) {
-            float by = 0.f;                            // the reference grows by this
+            float by = 0.f;                              // the reference grows by this
             bool first = false;
             if ((high >> (key >> 3)) & 1) {
-              const float mx = fmaxf(fmaxf(rs.red[0][key], rs.red[1][key]), fmaxf(rs.red[2][key], rs.red[3][key])) + rs.neg_m[key];
+              const float mx = fmaxf(fmaxf(rs.red[0][key], rs.red[1][key]), fmaxf(rs.red[2][key], rs.red[3][key]));
               first = rs.unset[key] && mx > -INFINITY;
               if (first || mx > kMax) by = mx - kTop;
             }
             rs.f[key] = first ? 0.f : ex2(-by);
+            rs.by[key] = -by;
             rs.neg_m[key] -= by;
             if (first) rs.unset[key] = 0;
             still = rs.unset[key];
           }
           unset_any = softmax_any(still);
 #pragma unroll
-          for (int r = 0; r < CH * 4; r++)
+          for (int r = 0; r < CH * 4; r++) {
             l[r] = mul2(l[r], *reinterpret_cast<const float2*>(&rs.f[2 * r]));
+            x[r] = add2(x[r], *reinterpret_cast<const float2*>(&rs.by[2 * r]));
+          }
           if (t > 0) {
             tc05_fence_after();
 #pragma unroll 1
@@ -925,12 +923,8 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
             }
             tmem_wait_st();
           }
-          softmax_sync();                              // f and high have been read
+          softmax_sync();                                // f, by and high have been read
         }
-        if (gone) break;
-        tc05_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s_free[gg & 1]));
         __syncwarp();
 #pragma unroll
         for (int ch = 0; ch < CH; ch++) {
@@ -1048,24 +1042,44 @@ __device__ __forceinline__ void load_floats(const float* p, float (&v)[N]) {
   }
 }
 
+// PER consecutive elements of a row as fp32 (16 bytes at a time where there are eight).
+template <typename T, int PER>
+__device__ __forceinline__ void load_row(const T* p, float (&v)[PER]) {
+  constexpr int WORDS = PER / 2;
+  uint32_t w[WORDS];
+  if constexpr (WORDS == 1) w[0] = *reinterpret_cast<const uint32_t*>(p);
+  else if constexpr (WORDS == 2) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+  else *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+#pragma unroll
+  for (int i = 0; i < WORDS; i++) {
+    const T* e = reinterpret_cast<const T*>(&w[i]);
+    v[2 * i] = row_f(e[0]), v[2 * i + 1] = row_f(e[1]);
+  }
+}
+
+// Latency-bound: three dependent rounds of loads (the call's numbers; queries and own rows; pieces), with the loads of
+// a round in flight together.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
   constexpr int PER = HD / 32;                         // columns per lane
+  constexpr int kOwn = 8, kAtOnce = 8;                 // own rows, pieces in flight
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const long long task = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  const int r = (int)(task % a.p.rc), pair = (int)(task / a.p.rc);
-  const int chunk = pair % a.p.chunks, head = pair / a.p.chunks % a.n_kv, b = pair / a.p.chunks / a.n_kv;
+  const unsigned task = blockIdx.x * kJoinWarps + (threadIdx.x >> 5), pair = task / (unsigned)a.p.rc;
+  const int r = (int)(task - pair * a.p.rc);
+  const int per_req = a.n_kv * a.p.chunks, b = (int)(pair / per_req), in_req = (int)pair - b * per_req;
+  const int head = in_req / a.p.chunks, chunk = in_req - head * a.p.chunks;
   if (b >= a.n_req) return;
+  const int total = a.units[a.n_req], first = a.units[b];
   const Request rq = request_of(a, read_request(a, b));
   const int rr = chunk * a.p.rc + r;
   if (rr >= rq.n * a.grp) return;
   const int i = rr / a.grp, qh = head * a.grp + rr % a.grp, row = rq.row0 + i;
-  const int total = a.units[a.n_req], ctas = min(a.grid, total);
+  const int ctas = min(a.grid, total);
   int c0 = 0, c1 = -1;                                 // CTAs that hold tiles of this row
   if (rq.tiles > 0) {
-    const long long s = a.units[b] + (long long)(head * rq.chunks + chunk) * rq.tiles, e = s + rq.tiles;
+    const long long s = first + (long long)(head * rq.chunks + chunk) * rq.tiles, e = s + rq.tiles;
     c0 = (int)(((s + 1) * ctas - 1) / total);
     c1 = (int)((e * ctas - 1) / total);
     if (c0 == c1 && !a.k_own) return;                  // written by the first kernel
@@ -1073,53 +1087,94 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
   float m = -INFINITY, L = 0.f, o[PER];
 #pragma unroll
   for (int c = 0; c < PER; c++) o[c] = 0.f;
-  auto take = [&](float mx, float w, const float (&v)[PER]) {   // add w (sum) and v at reference mx
-    const float mn = fmaxf(m, mx);
-    const float so = m == mn ? 1.f : ex2(m - mn), sn = mx == mn ? 1.f : ex2(mx - mn);
-    L = fmaf(w, sn, L * so);
+  // own rows [j0, j1): the first ones are on their way while the pieces are joined
+  float q[PER], k[kOwn][PER], v[kOwn][PER];
+  const int j1 = !a.k_own ? 0 : a.causal ? i + 1 : rq.n, j0 = a.causal && a.window > 0 ? max(0, i + 1 - a.window) : 0;
+  auto fetch = [&](int j) {
 #pragma unroll
-    for (int c = 0; c < PER; c++) o[c] = fmaf(v[c], sn, o[c] * so);
-    m = mn;
+    for (int u = 0; u < kOwn; u++) {
+      if (j + u >= j1) continue;
+      load_row<T, PER>(static_cast<const T*>(a.k_own) + (rq.row0 + j + u) * a.ko_row + head * a.ko_head + lane * PER, k[u]);
+      load_row<T, PER>(static_cast<const T*>(a.v_own) + (rq.row0 + j + u) * a.vo_row + head * a.vo_head + lane * PER, v[u]);
+    }
   };
-  constexpr int kAtOnce = 8;                           // pieces in flight
+  if (j0 < j1) {
+    load_row<T, PER>(static_cast<const T*>(a.q) + row * a.q_row + qh * a.q_head + lane * PER, q);
+    fetch(j0);
+  }
   for (int c = c0; c <= c1; c += kAtOnce) {
     float2 ml[kAtOnce];
-    float v[kAtOnce][PER];
+    float w[kAtOnce][PER], top = m;
 #pragma unroll
     for (int u = 0; u < kAtOnce; u++) {
       ml[u] = make_float2(kUnset, 0.f);
       if (c + u <= c1) {
         const size_t at = ((size_t)(c + u) + pair) * a.p.rp + r;
         ml[u] = __ldcg(&a.part_ml[at]);
-        load_floats<PER>(a.part_o + at * HD + lane * PER, v[u]);
+        load_floats<PER>(a.part_o + at * HD + lane * PER, w[u]);
       }
     }
 #pragma unroll
     for (int u = 0; u < kAtOnce; u++)
-      if (ml[u].x != kUnset) take(ml[u].x, ml[u].y, v[u]);
-  }
-  if (a.k_own) {
-    float q[PER];
-    const T* qp = static_cast<const T*>(a.q) + row * a.q_row + qh * a.q_head + lane * PER;
+      if (ml[u].x != kUnset) top = fmaxf(top, ml[u].x);
+    const float so = m == top ? 1.f : ex2(m - top);
+    L *= so;
 #pragma unroll
-    for (int j = 0; j < PER; j++) q[j] = row_f(qp[j]) * a.scale_log2;
-    const int j1 = a.causal ? i + 1 : rq.n, j0 = a.causal && a.window > 0 ? max(0, i + 1 - a.window) : 0;
-    for (int j = j0; j < j1; j++) {
-      const T* kp = static_cast<const T*>(a.k_own) + (rq.row0 + j) * a.ko_row + head * a.ko_head + lane * PER;
-      const T* vp = static_cast<const T*>(a.v_own) + (rq.row0 + j) * a.vo_row + head * a.vo_head + lane * PER;
-      float s = 0.f, v[PER];
+    for (int x = 0; x < PER; x++) o[x] *= so;
 #pragma unroll
-      for (int c = 0; c < PER; c++) {
-        s = fmaf(q[c], row_f(kp[c]), s);
-        v[c] = row_f(vp[c]);
-      }
-      take(warp_sum(s), 1.f, v);
+    for (int u = 0; u < kAtOnce; u++) {
+      if (ml[u].x == kUnset) continue;
+      const float sn = ml[u].x == top ? 1.f : ex2(ml[u].x - top);
+      L = fmaf(ml[u].y, sn, L);
+#pragma unroll
+      for (int x = 0; x < PER; x++) o[x] = fmaf(w[u][x], sn, o[x]);
     }
+    m = top;
+  }
+  for (int j = j0; j < j1; j += kOwn) {
+    if (j > j0) fetch(j);
+    float s8[8];
+#pragma unroll
+    for (int u = 0; u < kOwn; u++) {
+      s8[u] = 0.f;
+      if (j + u < j1) {
+#pragma unroll
+        for (int x = 0; x < PER; x++) s8[u] = fmaf(q[x], k[u][x], s8[u]);
+      }
+    }
+    // lane l: the score of row j + ((l >> 2) & 7)
+    float s = reduce8(s8, [](float x, float y) { return x + y; }) * a.scale_log2;
+    if (j + ((lane >> 2) & 7) >= j1) s = -INFINITY;
+    float top = s;
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    top = fmaxf(top, m);
+    const float p = s == -INFINITY ? 0.f : s == top ? 1.f : ex2(s - top), so = m == top ? 1.f : ex2(m - top);
+    float sum = p;
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    L = fmaf(L, so, sum);
+#pragma unroll
+    for (int x = 0; x < PER; x++) o[x] *= so;
+#pragma unroll
+    for (int u = 0; u < kOwn; u++) {
+      const float pu = __shfl_sync(0xffffffffu, p, 4 * u);
+      if (j + u < j1) {
+#pragma unroll
+        for (int x = 0; x < PER; x++) o[x] = fmaf(pu, v[u][x], o[x]);
+      }
+    }
+    m = top;
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
   T* out = static_cast<T*>(a.out) + row * a.o_row + qh * a.o_head + lane * PER;
 #pragma unroll
-  for (int c = 0; c < PER; c++) row_store(out + c, o[c] * inv);
+  for (int x = 0; x < PER; x += 2) {
+    T two[2];
+    row_store(&two[0], o[x] * inv);
+    row_store(&two[1], o[x + 1] * inv);
+    *reinterpret_cast<uint32_t*>(out + x) = *reinterpret_cast<const uint32_t*>(two);
+  }
 }
 
 template <typename T, int HD, int RP>
