@@ -1025,93 +1025,80 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
   }
 }
 
-// ---- the second kernel: join the pieces of a row, own rows, output; one warp per (request, head, row) --------
-constexpr int kJoinWarps = 4;
+// ---- the second kernel: join the pieces of a row, own rows, output ---------------------------------------------
+// Latency-bound: two dependent rounds of loads (the call's numbers; then queries, own rows and pieces together). A CTA
+// takes some rows of one (request, KV head, chunk), a row in HD / 8 lanes of eight columns each, so that the own
+// rows' K/V are read once for all of them (a warp per row, each reading them all, took 18 us instead of 6 for 32
+// requests x 5 rows of 5 query heads).
+constexpr int kJoinWarps = 8, kOwnTile = 16;           // own rows in shared memory at a time
+__host__ __device__ constexpr int join_rows(int hd) { return kJoinWarps * 256 / hd; }
 
-template <int N>
-__device__ __forceinline__ void load_floats(const float* p, float (&v)[N]) {
-  if constexpr (N == 2) {
-    const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
-    v[0] = x.x, v[1] = x.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(p + i));
-      v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
-    }
-  }
-}
-
-// PER consecutive elements of a row as fp32 (16 bytes at a time where there are eight).
-template <typename T, int PER>
-__device__ __forceinline__ void load_row(const T* p, float (&v)[PER]) {
-  constexpr int WORDS = PER / 2;
-  uint32_t w[WORDS];
-  if constexpr (WORDS == 1) w[0] = *reinterpret_cast<const uint32_t*>(p);
-  else if constexpr (WORDS == 2) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
-  else *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
-#pragma unroll
-  for (int i = 0; i < WORDS; i++) {
-    const T* e = reinterpret_cast<const T*>(&w[i]);
-    v[2 * i] = row_f(e[0]), v[2 * i + 1] = row_f(e[1]);
-  }
-}
-
-// Latency-bound: three dependent rounds of loads (the call's numbers; queries and own rows; pieces), with the loads of
-// a round in flight together.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
-  constexpr int PER = HD / 32;                         // columns per lane
-  constexpr int kOwn = 8, kAtOnce = 8;                 // own rows, pieces in flight
+  constexpr int LPR = HD / 8, kAtOnce = 4;             // lanes of a row; pieces in flight
+  constexpr int kStep = LPR / 8;                       // lanes between the scores of neighbouring own rows
+  constexpr int kLoads = kOwnTile * LPR / (kJoinWarps * 32) > 0 ? kOwnTile * LPR / (kJoinWarps * 32) : 1;
+  __shared__ uint4 own[2][kOwnTile][LPR];              // K, V
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const unsigned task = blockIdx.x * kJoinWarps + (threadIdx.x >> 5), pair = task / (unsigned)a.p.rc;
-  const int r = (int)(task - pair * a.p.rc);
-  const int per_req = a.n_kv * a.p.chunks, b = (int)(pair / per_req), in_req = (int)pair - b * per_req;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR;
+  const int pair = blockIdx.x, per_req = a.n_kv * a.p.chunks, b = pair / per_req, in_req = pair - b * per_req;
   const int head = in_req / a.p.chunks, chunk = in_req - head * a.p.chunks;
-  if (b >= a.n_req) return;
   const int total = a.units[a.n_req], first = a.units[b];
   const Request rq = request_of(a, read_request(a, b));
-  const int rr = chunk * a.p.rc + r;
-  if (rr >= rq.n * a.grp) return;
-  const int i = rr / a.grp, qh = head * a.grp + rr % a.grp, row = rq.row0 + i;
+  const int rows = min(a.p.rc, rq.n * a.grp - chunk * a.p.rc), r_cta = blockIdx.y * join_rows(HD);
+  if (r_cta >= rows) return;
   const int ctas = min(a.grid, total);
-  int c0 = 0, c1 = -1;                                 // CTAs that hold tiles of this row
+  int c0 = 0, c1 = -1;                                 // CTAs that hold tiles of these rows
   if (rq.tiles > 0) {
     const long long s = first + (long long)(head * rq.chunks + chunk) * rq.tiles, e = s + rq.tiles;
     c0 = (int)(((s + 1) * ctas - 1) / total);
     c1 = (int)((e * ctas - 1) / total);
     if (c0 == c1 && !a.k_own) return;                  // written by the first kernel
   }
-  float m = -INFINITY, L = 0.f, o[PER];
-#pragma unroll
-  for (int c = 0; c < PER; c++) o[c] = 0.f;
-  // own rows [j0, j1): the first ones are on their way while the pieces are joined
-  float q[PER], k[kOwn][PER], v[kOwn][PER];
-  const int j1 = !a.k_own ? 0 : a.causal ? i + 1 : rq.n, j0 = a.causal && a.window > 0 ? max(0, i + 1 - a.window) : 0;
+  const int r = min(r_cta + warp * (32 / LPR) + lane / LPR, rows - 1);    // spare lanes repeat the last row
+  const bool live = r == r_cta + warp * (32 / LPR) + lane / LPR;
+  const int rr = chunk * a.p.rc + r, i = rr / a.grp, qh = head * a.grp + rr - i * a.grp, row = rq.row0 + i;
+  const int n_own = a.k_own ? rq.n : 0;
+  // own rows of a tile: this thread's pieces on their way, then into shared memory
+  uint4 kw[kLoads], vw[kLoads];
   auto fetch = [&](int j) {
 #pragma unroll
-    for (int u = 0; u < kOwn; u++) {
-      if (j + u >= j1) continue;
-      load_row<T, PER>(static_cast<const T*>(a.k_own) + (rq.row0 + j + u) * a.ko_row + head * a.ko_head + lane * PER, k[u]);
-      load_row<T, PER>(static_cast<const T*>(a.v_own) + (rq.row0 + j + u) * a.vo_row + head * a.vo_head + lane * PER, v[u]);
+    for (int u = 0; u < kLoads; u++) {
+      const int at = threadIdx.x + u * kJoinWarps * 32, jr = at / LPR, c = at % LPR;
+      kw[u] = vw[u] = make_uint4(0, 0, 0, 0);
+      if (jr < kOwnTile && j + jr < n_own) {
+        kw[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k_own) + (rq.row0 + j + jr) * a.ko_row + head * a.ko_head + c * 8);
+        vw[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v_own) + (rq.row0 + j + jr) * a.vo_row + head * a.vo_head + c * 8);
+      }
     }
   };
-  if (j0 < j1) {
-    load_row<T, PER>(static_cast<const T*>(a.q) + row * a.q_row + qh * a.q_head + lane * PER, q);
-    fetch(j0);
+  auto unpack = [](uint4 w, float (&v)[8]) {
+    const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+    for (int x = 0; x < 8; x++) v[x] = row_f(e[x]);
+  };
+  float q[8];
+  if (n_own > 0) {
+    fetch(0);
+    unpack(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + row * a.q_row + qh * a.q_head + sub * 8), q);
   }
+  float m = -INFINITY, L = 0.f, o[8];
+#pragma unroll
+  for (int c = 0; c < 8; c++) o[c] = 0.f;
   for (int c = c0; c <= c1; c += kAtOnce) {
     float2 ml[kAtOnce];
-    float w[kAtOnce][PER], top = m;
+    float4 w[kAtOnce][2];
+    float top = m;
 #pragma unroll
     for (int u = 0; u < kAtOnce; u++) {
       ml[u] = make_float2(kUnset, 0.f);
       if (c + u <= c1) {
         const size_t at = ((size_t)(c + u) + pair) * a.p.rp + r;
         ml[u] = __ldcg(&a.part_ml[at]);
-        load_floats<PER>(a.part_o + at * HD + lane * PER, w[u]);
+        const float4* p = reinterpret_cast<const float4*>(a.part_o + at * HD + sub * 8);
+        w[u][0] = __ldcg(p);
+        w[u][1] = __ldcg(p + 1);
       }
     }
 #pragma unroll
@@ -1120,61 +1107,87 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
     const float so = m == top ? 1.f : ex2(m - top);
     L *= so;
 #pragma unroll
-    for (int x = 0; x < PER; x++) o[x] *= so;
+    for (int x = 0; x < 8; x++) o[x] *= so;
 #pragma unroll
     for (int u = 0; u < kAtOnce; u++) {
       if (ml[u].x == kUnset) continue;
       const float sn = ml[u].x == top ? 1.f : ex2(ml[u].x - top);
+      const float v[8] = {w[u][0].x, w[u][0].y, w[u][0].z, w[u][0].w, w[u][1].x, w[u][1].y, w[u][1].z, w[u][1].w};
       L = fmaf(ml[u].y, sn, L);
 #pragma unroll
-      for (int x = 0; x < PER; x++) o[x] = fmaf(w[u][x], sn, o[x]);
+      for (int x = 0; x < 8; x++) o[x] = fmaf(v[x], sn, o[x]);
     }
     m = top;
   }
-  for (int j = j0; j < j1; j += kOwn) {
-    if (j > j0) fetch(j);
-    float s8[8];
+  const int j1 = a.causal ? i + 1 : n_own, j0 = a.causal && a.window > 0 ? max(0, i + 1 - a.window) : 0;   // own rows it sees
+  for (int t0 = 0; t0 < n_own; t0 += kOwnTile) {
+    if (t0 > 0) {
+      __syncthreads();                                 // the tile before has been read
+      fetch(t0);
+    }
 #pragma unroll
-    for (int u = 0; u < kOwn; u++) {
-      s8[u] = 0.f;
-      if (j + u < j1) {
-#pragma unroll
-        for (int x = 0; x < PER; x++) s8[u] = fmaf(q[x], k[u][x], s8[u]);
+    for (int u = 0; u < kLoads; u++) {
+      const int at = threadIdx.x + u * kJoinWarps * 32;
+      if (at < kOwnTile * LPR) {
+        own[0][at / LPR][at % LPR] = kw[u];
+        own[1][at / LPR][at % LPR] = vw[u];
       }
     }
-    // lane l: the score of row j + ((l >> 2) & 7)
-    float s = reduce8(s8, [](float x, float y) { return x + y; }) * a.scale_log2;
-    if (j + ((lane >> 2) & 7) >= j1) s = -INFINITY;
-    float top = s;
+    __syncthreads();
+#pragma unroll 1
+    for (int j = t0; j < min(t0 + kOwnTile, n_own); j += 8) {
+      float s8[8];
 #pragma unroll
-    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    top = fmaxf(top, m);
-    const float p = s == -INFINITY ? 0.f : s == top ? 1.f : ex2(s - top), so = m == top ? 1.f : ex2(m - top);
-    float sum = p;
+      for (int u = 0; u < 8; u++) {
+        float k[8];
+        unpack(own[0][j - t0 + u][sub], k);
+        s8[u] = 0.f;
 #pragma unroll
-    for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    L = fmaf(L, so, sum);
-#pragma unroll
-    for (int x = 0; x < PER; x++) o[x] *= so;
-#pragma unroll
-    for (int u = 0; u < kOwn; u++) {
-      const float pu = __shfl_sync(0xffffffffu, p, 4 * u);
-      if (j + u < j1) {
-#pragma unroll
-        for (int x = 0; x < PER; x++) o[x] = fmaf(pu, v[u][x], o[x]);
+        for (int x = 0; x < 8; x++) s8[u] = fmaf(q[x], k[x], s8[u]);
       }
+      // over the row's lanes; lane l of them: the score of row j + l / kStep
+      float h4[4], h2[2];
+      constexpr int D = LPR / 2;
+#pragma unroll
+      for (int x = 0; x < 4; x++) h4[x] = (sub & D ? s8[x + 4] : s8[x]) + __shfl_xor_sync(0xffffffffu, sub & D ? s8[x] : s8[x + 4], D);
+#pragma unroll
+      for (int x = 0; x < 2; x++) h2[x] = (sub & (D / 2) ? h4[x + 2] : h4[x]) + __shfl_xor_sync(0xffffffffu, sub & (D / 2) ? h4[x] : h4[x + 2], D / 2);
+      float s = (sub & (D / 4) ? h2[1] : h2[0]) + __shfl_xor_sync(0xffffffffu, sub & (D / 4) ? h2[0] : h2[1], D / 4);
+#pragma unroll
+      for (int d = kStep / 2; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+      const int mine = j + sub / kStep;
+      s = mine >= j0 && mine < j1 ? s * a.scale_log2 : -INFINITY;
+      float top = s;
+#pragma unroll
+      for (int d = kStep; d < LPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      top = fmaxf(top, m);
+      const float base = top == -INFINITY ? 0.f : top;
+      const float p = ex2(s - base), so = ex2(m - base);
+      float sum = p;
+#pragma unroll
+      for (int d = kStep; d < LPR; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      L = fmaf(L, so, sum);
+#pragma unroll
+      for (int x = 0; x < 8; x++) o[x] *= so;
+#pragma unroll
+      for (int u = 0; u < 8; u++) {
+        const float pu = __shfl_sync(0xffffffffu, p, (lane - sub) + u * kStep);
+        if (j + u < j0 || j + u >= j1) continue;       // a masked row's values may be anything
+        float v[8];
+        unpack(own[1][j - t0 + u][sub], v);
+#pragma unroll
+        for (int x = 0; x < 8; x++) o[x] = fmaf(pu, v[x], o[x]);
+      }
+      m = top;
     }
-    m = top;
   }
+  if (!live) return;
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  T* out = static_cast<T*>(a.out) + row * a.o_row + qh * a.o_head + lane * PER;
+  uint4 w;
+  T* e = reinterpret_cast<T*>(&w);
 #pragma unroll
-  for (int x = 0; x < PER; x += 2) {
-    T two[2];
-    row_store(&two[0], o[x] * inv);
-    row_store(&two[1], o[x + 1] * inv);
-    *reinterpret_cast<uint32_t*>(out + x) = *reinterpret_cast<const uint32_t*>(two);
-  }
+  for (int x = 0; x < 8; x++) row_store(&e[x], o[x] * inv);
+  *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * a.o_row + qh * a.o_head + sub * 8) = w;
 }
 
 template <typename T, int HD, int RP>
@@ -1191,8 +1204,8 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtens
   }
   e = launch_pdl(cache_attn_kernel<T, HD, RP>, dim3(a.grid), dim3(kThreads), a.p.smem, s, a, kmap, vmap);
   if (e != cudaSuccess) return e;
-  const long long tasks = (long long)a.n_req * a.n_kv * a.p.chunks * a.p.rc;
-  return launch_pdl(cache_attn_join_kernel<T, HD>, dim3((unsigned)((tasks + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, s, a);
+  const dim3 join_grid(a.n_req * a.n_kv * a.p.chunks, (a.p.rc + join_rows(HD) - 1) / join_rows(HD));
+  return launch_pdl(cache_attn_join_kernel<T, HD>, join_grid, dim3(kJoinWarps * 32), 0, s, a);
 }
 
 template <typename T, int HD>
