@@ -35,6 +35,7 @@ class DraftConfig:
     markov_rank: int = 0          # Markov sequential head rank r (0: none), a multiple of 64
     large_batch_tc05: bool = False  # many-row draft calls on the tcgen05 contraction (library option)
     skinny_tc05: bool = False     # draft calls of <= 32 rows on the tcgen05 projection kernel (library option)
+    cache_blocks: int = 0         # > 0: context K/V in a paged 8-bit cache of that many 64-token blocks (library option)
     append_min: int = 0           # new context rows per request per round (0,0: gamma rows)
     append_max: int = 0
     ctx_min: int = 0              # ragged contexts: P uniform in [ctx_min, ctx_len] (0: fixed)

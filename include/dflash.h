@@ -112,6 +112,14 @@ typedef struct {
                          and (d == H) the LM head each as one tcgen05 launch with the same fused
                          epilogues: weights dequantised to f16 (one rounding) in shared memory,
                          fp32 accumulators in tensor memory. */
+  int cache_blocks;   /* 0: the context K/V of each request slot in an f16 ring of ctx_capacity rows. N > 0
+                         (adtype DFLASH_BF16): in the paged 8-bit cache (dflash_cache below): N blocks of
+                         64 tokens, e4m3 with one scale per block and KV head, that all requests share,
+                         so the workspace follows the context that requests have and not max_batch times
+                         the longest, at half the bytes a row. A request takes a block per 64
+                         positions, at most ceil(window / 64) + 1 with a window; dflash_project_ctx
+                         returns DFLASH_ECAPACITY when too few are free, dflash_reset_request frees a
+                         request's blocks. Attention then reads rounded K/V (4 significant bits). */
 } dflash_config;
 
 typedef struct {
@@ -471,6 +479,12 @@ typedef struct {
  * cores as sums of e4m3 values, 8 significant bits for bf16 rows and 11 for f16 rows (the format's own
  * precision); products accumulate in fp32, softmax sums and outputs are fp32 and rounded once. */
 int dflash_cache_attention(dflash_cache* c, const dflash_attention* a, void* stream);
+
+/* The paged context cache of a handle made with cache_blocks > 0, for inspection and for moving contexts: its codes,
+ * scales and limits (*cache) and its block tables (*pool; a request's context length is pool->lens[slot]
+ * once the calls before have run). The memory is the handle's workspace: reading is ordered after the handle's calls
+ * on its stream, and writing it is the caller's own risk. Returns DFLASH_EINVAL for a handle without one. */
+int dflash_ctx_cache(const dflash_handle* h, dflash_cache_config* cache, dflash_pool* pool);
 
 
 /* Allocation-free greedy token and softmax confidence for logits the caller already holds.

@@ -89,7 +89,7 @@ class dflash_config(ctypes.Structure):
         "gamma", "window", "max_batch", "ctx_capacity")] + \
         [("eps", ctypes.c_float), ("wdtype", ctypes.c_int), ("adtype", ctypes.c_int), ("ffn_act", ctypes.c_int),
          ("draft_all_rows", ctypes.c_int), ("markov_rank", ctypes.c_int), ("large_batch_tc05", ctypes.c_int),
-         ("skinny_tc05", ctypes.c_int)]
+         ("skinny_tc05", ctypes.c_int), ("cache_blocks", ctypes.c_int)]
 
 
 class dflash_matrix(ctypes.Structure):
@@ -157,7 +157,7 @@ SYMBOLS = ["dflash_workspace_bytes", "dflash_create", "dflash_project_ctx", "dfl
            "dflash_accept_kept", "dflash_rows_matmul_plan", "dflash_rows_matmul", "dflash_set_wait_limit",
            "dflash_debug_stall", "dflash_accept_histogram", "dflash_cache_workspace_bytes", "dflash_cache_create",
            "dflash_cache_destroy", "dflash_cache_check_errors", "dflash_pool_reserve", "dflash_pool_truncate",
-           "dflash_cache_append", "dflash_cache_attention"]
+           "dflash_cache_append", "dflash_cache_attention", "dflash_ctx_cache"]
 
 
 def lib():
@@ -228,6 +228,8 @@ def lib():
         L.dflash_cache_append.argtypes = [vp, i32, i32, i32, vp, P(dflash_rows), P(dflash_rows), i32, vp]
         L.dflash_cache_attention.restype = i32
         L.dflash_cache_attention.argtypes = [vp, P(dflash_attention), vp]
+        L.dflash_ctx_cache.restype = i32
+        L.dflash_ctx_cache.argtypes = [vp, P(dflash_cache_config), P(dflash_pool)]
         _lib = L
     return _lib
 
@@ -285,7 +287,7 @@ def make_config(cfg, max_batch: int | None = None, ctx_capacity: int | None = No
                          cfg.target_hidden, cfg.vocab, cfg.gamma, cfg.window, mb, ctx_capacity, cfg.eps,
                          DTYPE[cfg.wdtype], DTYPE[cfg.adtype], FFN[cfg.ffn], 1 if cfg.draft_all_rows else 0,
                          cfg.markov_rank, 1 if getattr(cfg, "large_batch_tc05", False) else 0,
-                         1 if getattr(cfg, "skinny_tc05", False) else 0)
+                         1 if getattr(cfg, "skinny_tc05", False) else 0, getattr(cfg, "cache_blocks", 0))
 
 
 class DeviceModel:
@@ -387,6 +389,25 @@ class Handle:
         return _check(lib().dflash_accept_kept(self.h, draft.shape[0], draft.data_ptr(), keep.data_ptr(),
                                                target.data_ptr(), accept_len.data_ptr(), next_anchor.data_ptr(),
                                                _stream_ptr(stream)), "dflash_accept_kept")
+
+    def ctx_cache(self):
+        """The paged context cache of a handle with cache_blocks > 0 as tensors on the handle's workspace: codes
+        k, v uint8 [layers][blocks][KV heads][64][head_dim], scales fp32 [layers][blocks][KV heads], lens int32
+        [max_batch] and table int32 [max_batch][blocks per request]."""
+        import torch
+        c, p = dflash_cache_config(), dflash_pool()
+        _check(lib().dflash_ctx_cache(self.h, ctypes.byref(c), ctypes.byref(p)), "dflash_ctx_cache")
+
+        def view(ptr, dtype, *shape):
+            n = torch.Size(shape).numel() * torch.empty((), dtype=dtype).element_size()
+            at = ptr - self.workspace.data_ptr()
+            return self.workspace[at:at + n].view(dtype).view(shape)
+
+        codes = (c.n_layers, c.n_blocks, c.n_kv_heads, c.block_tokens, c.head_dim)
+        return {"k": view(c.k, torch.uint8, *codes), "v": view(c.v, torch.uint8, *codes),
+                "k_scale": view(c.k_scale, torch.float32, *codes[:3]), "v_scale": view(c.v_scale, torch.float32, *codes[:3]),
+                "lens": view(p.lens, torch.int32, p.table_rows), "table": view(p.table, torch.int32, p.table_rows, p.table_blocks),
+                "free_count": view(p.free_count, torch.int32, 1)}
 
     def reset_request(self, req_id: int) -> int:
         return _check(lib().dflash_reset_request(self.h, req_id), "dflash_reset_request")

@@ -10,6 +10,7 @@
 #include <new>
 
 #include "gemm_tc05.h"
+#include "cache.h"
 #include "internal.h"
 
 using namespace dfl;
@@ -71,6 +72,16 @@ struct dflash_handle {
   int pj_on = 0;
   float* pj_partials = nullptr;  // [n_sm][2][32][128] pieces of tiles cut between CTAs
   CUtensorMap kmap{}, vmap{};
+  // context K/V in the paged 8-bit cache (config cache_blocks); kc, vc are then the f16 rows of one projection
+  // chunk, [L][Hkv][xw_rows][hd], on their way into it
+  dflash_cache* cache = nullptr;
+  dflash_cache_config cache_cfg{};
+  dflash_pool pool{};
+  uint8_t* cache_ws = nullptr;
+  size_t cache_ws_bytes = 0;
+  int table_blocks = 0;
+  int32_t *pool_req = nullptr, *pool_n = nullptr, *pool_slots = nullptr, *pool_start = nullptr, *pool_granted = nullptr;
+  bool reset_pending[DFLASH_MAX_BATCH] = {};   // slots whose blocks go back with the next call
 
   int64_t ctx_len[DFLASH_MAX_BATCH] = {};
   dflash_stats stats{};
@@ -182,6 +193,7 @@ bool valid_config(const dflash_config* c) {
   if (c->markov_rank < 0 || c->markov_rank > 1024 || c->markov_rank % 64) return false;
   if (c->large_batch_tc05 != 0 && c->large_batch_tc05 != 1) return false;
   if (c->skinny_tc05 != 0 && c->skinny_tc05 != 1) return false;
+  if (c->cache_blocks < 0 || c->cache_blocks > (1 << 24) || (c->cache_blocks > 0 && c->adtype != DFLASH_BF16)) return false;
   if (c->wdtype < DFLASH_F32 || c->wdtype > DFLASH_Q4G64) return false;
   if (c->adtype == DFLASH_F32) {
     if (c->wdtype != DFLASH_F32) return false;
@@ -216,6 +228,59 @@ Tc05Plan plan_kv_tc05(const dflash_handle* h, int rows) {
                    std::max(1, h->n_sm / std::max(1, h->L)));
 }
 
+// The paged cache of the context: codes and scales of every layer, tables and the pool's state.
+constexpr int kCtxBlock = 64;
+void carve_cache(dflash_handle* h, Carver& cv) {
+  const dflash_config& c = h->cfg;
+  const int nb = c.cache_blocks;
+  // with a window the table is a ring: the blocks that a window can touch
+  h->table_blocks = ((c.window > 0 ? c.window : c.ctx_capacity) + kCtxBlock - 1) / kCtxBlock + (c.window > 0 ? 1 : 0);
+  dflash_cache_config& f = h->cache_cfg;
+  f.n_layers = h->L;
+  f.n_blocks = nb;
+  f.block_tokens = kCtxBlock;
+  f.n_kv_heads = c.n_kv_heads;
+  f.head_dim = c.head_dim;
+  f.token_stride = c.head_dim;
+  f.head_stride = (int64_t)kCtxBlock * c.head_dim;
+  f.block_stride = f.head_stride * c.n_kv_heads;
+  f.layer_stride = f.block_stride * nb;
+  f.n_q_heads = c.n_q_heads;
+  f.max_requests = c.max_batch;
+  f.max_q = h->G;
+  const size_t codes = (size_t)f.layer_stride * h->L, scales = (size_t)h->L * nb * c.n_kv_heads * 4;
+  f.k = cv.take<void>(codes);
+  f.v = cv.take<void>(codes);
+  f.k_scale = cv.take<float>(scales);
+  f.v_scale = cv.take<float>(scales);
+  // the addresses do not change the size: any aligned one passes the checks while only sizes are computed
+  dflash_cache_config probe = f;
+  if (!cv.base) probe.k = probe.v = probe.k_scale = probe.v_scale = reinterpret_cast<float*>(256);
+  h->cache_ws_bytes = dflash_cache_workspace_bytes(&probe);
+  h->cache_ws = cv.take<uint8_t>(h->cache_ws_bytes);
+  h->pool.block_tokens = kCtxBlock;
+  h->pool.n_blocks = nb;
+  h->pool.table_rows = c.max_batch;
+  h->pool.table_blocks = h->table_blocks;
+  h->pool.ring = c.window > 0;
+  h->pool.lens = cv.take<int32_t>((size_t)c.max_batch * 4);
+  h->pool.table = cv.take<int32_t>((size_t)c.max_batch * h->table_blocks * 4);
+  h->pool.free_list = cv.take<int32_t>((size_t)nb * 4);
+  h->pool.free_count = cv.take<int32_t>(4);
+  h->pool.scratch = cv.take<uint8_t>(DFLASH_POOL_SCRATCH);
+  h->pool_req = cv.take<int32_t>(DFLASH_MAX_BATCH * 4);
+  h->pool_n = cv.take<int32_t>(DFLASH_MAX_BATCH * 4);
+  h->pool_granted = cv.take<int32_t>(DFLASH_MAX_BATCH * 4);
+  h->pool_start = cv.take<int32_t>((DFLASH_MAX_BATCH + 1) * 4);
+  h->pool_slots = cv.take<int32_t>((size_t)h->xw_rows * 4);
+}
+
+// Blocks that a request of `len` tokens holds.
+int64_t ctx_blocks(const dflash_handle* h, int64_t len) {
+  const int64_t b = (len + kCtxBlock - 1) / kCtxBlock;
+  return h->cfg.window > 0 ? std::min<int64_t>(b, h->table_blocks) : b;
+}
+
 size_t carve(dflash_handle* h, uint8_t* base) {
   const dflash_config& c = h->cfg;
   Carver cv{base};
@@ -248,9 +313,16 @@ size_t carve(dflash_handle* h, uint8_t* base) {
   h->attn_norm = cv.take<float>((size_t)h->L * h->d * 4);
   h->ff_norm = cv.take<float>((size_t)h->L * h->d * 4);
   const size_t state_begin = round_up(cv.off, 256);
-  const size_t cache_elems = (size_t)h->L * c.max_batch * c.n_kv_heads * h->cap * c.head_dim;
+  // a context call on the tcgen05 contraction projects up to kTcMaxRows rows' context K/V of every
+  // layer in one grouped launch, from one input plane per layer
+  const bool tc_possible = c.large_batch_tc05 && h->fmt == FMT_Q4 && !h->act_f32 && h->d == h->H && !c.markov_rank &&
+                           std::min(c.max_batch * h->G, kTcMaxRows) > kMaxRows;
+  h->xw_rows = tc_possible ? kTcMaxRows : kMaxCtxChunk;
+  const size_t kv_rows = c.cache_blocks ? (size_t)h->xw_rows : (size_t)c.max_batch * h->cap;
+  const size_t cache_elems = (size_t)h->L * c.n_kv_heads * kv_rows * c.head_dim;
   h->kc = cv.take<void>(cache_elems * ab);
   h->vc = cv.take<void>(cache_elems * ab);
+  if (c.cache_blocks) carve_cache(h, cv);
   const int R = h->r_blk;
   h->h = cv.take<float>((size_t)R * h->d * 4);
   h->xn = cv.take<void>((size_t)R * h->d * ab * 2);   // f16 values, then their f16 remainders
@@ -264,11 +336,6 @@ size_t carve(dflash_handle* h, uint8_t* base) {
   h->tokrow = cv.take<float>((size_t)c.max_batch * h->d * 4);
   h->ssq_ld = (h->d + 15) / 16;
   h->ssq = cv.take<float>((size_t)R * h->ssq_ld * 4);
-  // a context call on the tcgen05 contraction projects up to kTcMaxRows rows' context K/V of every
-  // layer in one grouped launch, from one input plane per layer
-  const bool tc_possible = c.large_batch_tc05 && h->fmt == FMT_Q4 && !h->act_f32 && h->d == h->H && !c.markov_rank &&
-                           std::min(c.max_batch * h->G, kTcMaxRows) > kMaxRows;
-  h->xw_rows = tc_possible ? kTcMaxRows : kMaxCtxChunk;
   h->ssq_ctx = cv.take<float>((size_t)h->xw_rows * h->ssq_ld * 2 * 4);
   h->xw = cv.take<void>((size_t)h->L * h->xw_rows * h->d * ab * 2);
   if (c.markov_rank) {
@@ -715,6 +782,40 @@ int run_tc05_kv(dflash_handle* h, int rows, const GemvCall* calls, const int* r0
                                         layer_bytes / 4, s));
 }
 
+// Blocks of requests that dflash_reset_request has ended go back to the pool.
+int release_blocks(dflash_handle* h, cudaStream_t s) {
+  if (!h->cache) return DFLASH_OK;
+  PoolNumbers v{};
+  for (int r = 0; r < h->cfg.max_batch; r++)
+    if (h->reset_pending[r]) v.req[v.n_req++] = r;   // to length 0
+  if (v.n_req == 0) return DFLASH_OK;
+  h->launches += 2;
+  int st = status_of(launch_pool_numbers(v, h->pool_req, h->pool_n, s));
+  if (!st) st = dflash_pool_truncate(&h->pool, v.n_req, h->pool_req, h->pool_n, s);
+  if (st) return st;
+  std::fill(h->reset_pending, h->reset_pending + DFLASH_MAX_BATCH, false);
+  return DFLASH_OK;
+}
+
+// Take the blocks for a projection chunk's rows and quantise its f16 K/V rows of every layer into them. The numbers of
+// the chunk are cleared for the next one.
+int append_chunk(dflash_handle* h, PoolNumbers& v, int rows, int stage_rows, cudaStream_t s) {
+  const dflash_config& c = h->cfg;
+  dflash_rows k{}, vv{};
+  k.data = h->kc;
+  vv.data = h->vc;
+  k.row_stride = vv.row_stride = c.head_dim;
+  k.head_stride = vv.head_stride = (int64_t)stage_rows * c.head_dim;
+  k.layer_stride = vv.layer_stride = (int64_t)c.n_kv_heads * stage_rows * c.head_dim;
+  h->launches += 3;
+  int st = status_of(launch_pool_numbers(v, h->pool_req, h->pool_n, s));
+  if (!st) st = dflash_pool_reserve(&h->pool, v.n_req, h->pool_req, h->pool_n, h->pool_slots, rows, h->pool_start, h->pool_granted, s);
+  if (!st) st = dflash_cache_append(h->cache, 0, h->L, rows, h->pool_slots, &k, &vv, DFLASH_F16, s);
+  v.n_req = 0;
+  return st;
+}
+
+
 // One projection of a draft call of at most kProjMaxRows block rows on the tcgen05 projection
 // kernel: the contraction runs over rows [0, rows) of x (f16 [rows][ldx], the f16 remainder at
 // element offset lo_off when nonzero); the epilogue (described as for run_gemv) reads contraction
@@ -870,12 +971,15 @@ int dflash_create(const dflash_config* cfg, const dflash_weights* w, void* works
   chk(status_of(cudaMemcpyAsync(h->block_pos, w->block_pos, (size_t)h->G * h->d * 4, cudaMemcpyDefault, s)));
   chk(status_of(cudaMemcpyAsync(h->out_norm, w->out_norm, h->d * 4, cudaMemcpyDefault, s)));
   h->embed = w->embed;
-  if (!h->act_f32 && st == DFLASH_OK) {
+  if (cfg->cache_blocks) {
+    if (st == DFLASH_OK) st = dflash_cache_create(&h->cache_cfg, h->cache_ws, h->cache_ws_bytes, stream, &h->cache);
+    chk(status_of(launch_pool_init(cfg->cache_blocks, h->pool.free_list, h->pool.free_count, s)));
+  } else if (!h->act_f32 && st == DFLASH_OK) {
     chk(make_cache_map(h, h->kc, &h->kmap));
     chk(make_cache_map(h, h->vc, &h->vmap));
   }
   if (st != DFLASH_OK) {
-    delete h;
+    dflash_destroy(h);
     return st;
   }
   *out = h;
@@ -898,11 +1002,28 @@ int dflash_project_ctx(dflash_handle* h, int n_req, const int32_t* req_ids, cons
   }
   if (total == 0) return DFLASH_OK;
   if (!taps) return DFLASH_EINVAL;
+  if (h->cache) {   // the blocks that all requests hold after this call
+    int64_t len[DFLASH_MAX_BATCH], blocks = 0;
+    for (int r = 0; r < h->cfg.max_batch; r++) len[r] = h->ctx_len[r];
+    for (int i = 0; i < n_req; i++) len[req_ids[i]] += n_new[i];
+    for (int r = 0; r < h->cfg.max_batch; r++) {
+      if (len[r] >= 0x7fff0000) return DFLASH_ECAPACITY;   // positions are 32-bit there
+      blocks += ctx_blocks(h, len[r]);
+    }
+    if (blocks > h->cfg.cache_blocks) return DFLASH_ECAPACITY;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  {
+    const int st = release_blocks(h, s);
+    if (st) return st;
+  }
   const size_t ab = h->act_bytes;
   const uint8_t* tp = static_cast<const uint8_t*>(taps);
   const int parts = h->ssq_ld;
-  const size_t layer_cache = (size_t)h->cfg.max_batch * h->cfg.n_kv_heads * h->cap * h->cfg.head_dim * ab;
+  // the paged cache takes a projection chunk's rows from the f16 rows that the ring would have held
+  const int cap = h->cache ? h->xw_rows : h->cap, planes = h->cache ? 1 : h->cfg.max_batch;
+  const size_t layer_cache = (size_t)planes * h->cfg.n_kv_heads * cap * h->cfg.head_dim * ab;
+  PoolNumbers chunk_of{};
 
   // rows in call order: (slot, position)
   int req_i = 0, j_in = 0;
@@ -914,7 +1035,7 @@ int dflash_project_ctx(dflash_handle* h, int n_req, const int32_t* req_ids, cons
   // ring within the call (later rows must overwrite earlier ones in order: the chunked path then)
   int max_new = 0;
   for (int i = 0; i < n_req; i++) max_new = std::max(max_new, (int)n_new[i]);
-  const bool tc_kv = tc && max_new <= h->cap;
+  const bool tc_kv = tc && (h->cache || max_new <= h->cap);
   Tc05Plan wcp{};
   int64_t tc_row0 = 0;
   int tc_rows = 0;
@@ -941,6 +1062,16 @@ int dflash_project_ctx(dflash_handle* h, int n_req, const int32_t* req_ids, cons
       }
       slots[r] = req_ids[req_i];
       pos[r] = (int)((h->ctx_len[req_ids[req_i]] + j_in) % h->cap);
+      if (h->cache) {
+        const int n = chunk_of.n_req;
+        if (n == 0 || chunk_of.req[n - 1] != slots[r]) {
+          chunk_of.req[chunk_of.n_req] = slots[r];
+          chunk_of.n[chunk_of.n_req++] = 0;
+        }
+        chunk_of.n[chunk_of.n_req - 1]++;
+        slots[r] = 0;
+        pos[r] = (tc_kv ? (int)(row - tc_row0) : 0) + r;
+      }
       j_in++;
     }
     // Eq 2: x = W_c taps; epilogue writes x*ctx_norm*attn_norm_i for every layer + sums of squares
@@ -1001,7 +1132,7 @@ int dflash_project_ctx(dflash_handle* h, int n_req, const int32_t* req_ids, cons
       c2.e.n_rows = 2 * h->kvd;
       c2.e.kc = static_cast<uint8_t*>(h->kc) + i * layer_cache;
       c2.e.vc = static_cast<uint8_t*>(h->vc) + i * layer_cache;
-      c2.e.cap = h->cap;
+      c2.e.cap = cap;
       c2.e.hd = h->cfg.head_dim;
       c2.e.n_kv = h->cfg.n_kv_heads;
       c2.e.kvd = h->kvd;
@@ -1018,6 +1149,7 @@ int dflash_project_ctx(dflash_handle* h, int n_req, const int32_t* req_ids, cons
         if (row + rc == tc_row0 + tc_rows) {
           probe_begin(h, DFLASH_PROBE_CTX_KV, s);
           st = run_tc05_kv(h, tc_rows, kv_calls, kv_r0, n_kv, s);
+          if (!st && h->cache) st = append_chunk(h, chunk_of, tc_rows, cap, s);
           if (st) return st;
           probe_end(h, DFLASH_PROBE_CTX_KV, s);
         }
@@ -1025,6 +1157,7 @@ int dflash_project_ctx(dflash_handle* h, int n_req, const int32_t* req_ids, cons
       }
       probe_begin(h, DFLASH_PROBE_CTX_KV, s);
       st = run_gemv(h, c2, s);
+      if (!st && h->cache) st = append_chunk(h, chunk_of, rc, cap, s);
       if (st) return st;
       probe_end(h, DFLASH_PROBE_CTX_KV, s);
     }
@@ -1061,6 +1194,15 @@ int dflash_draft_block(dflash_handle* h, int n_req, const int32_t* req_ids, cons
     ~StallScope() { h->stall_active = 0; }
   } stall_scope(h);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (h->cache) {
+    int st = release_blocks(h, s);
+    if (st) return st;
+    PoolNumbers v{};
+    v.n_req = n_req;
+    std::copy(req_ids, req_ids + n_req, v.req);
+    h->launches++;
+    if ((st = status_of(launch_pool_numbers(v, h->pool_req, nullptr, s)))) return st;
+  }
   const dflash_config& c = h->cfg;
   const size_t ab = h->act_bytes;
   const int G = h->G, n = h->nd, d = h->d;   // n drafting rows per request: the last n block rows
@@ -1175,7 +1317,29 @@ int dflash_draft_block(dflash_handle* h, int n_req, const int32_t* req_ids, cons
     if ((st = flush())) return st;
     if (i == 0) probe_end(h, DFLASH_PROBE_QKV, s);
     // attention over [windowed context ++ block], no causal mask
-    {
+    if (h->cache) {
+      dflash_attention ca{};
+      ca.layer = i;
+      ca.n_requests = n_req;
+      ca.n_rows = rows_all;
+      ca.max_q = G;
+      ca.table_rows = c.max_batch;
+      ca.table_blocks = h->table_blocks;
+      ca.requests = h->pool_req;
+      ca.lens = h->pool.lens;
+      ca.table = h->pool.table;
+      ca.dtype = DFLASH_F16;
+      ca.q = dflash_rows{h->q, 0, h->qd, c.head_dim};
+      ca.out = dflash_rows{h->attn, 0, h->qd, c.head_dim};
+      ca.k_own = dflash_rows{h->kb, 0, h->kvd, c.head_dim};
+      ca.v_own = dflash_rows{h->vb, 0, h->kvd, c.head_dim};
+      ca.window = c.window;
+      ca.scale = (float)(1.0 / sqrt((double)c.head_dim));
+      if (i == 0) probe_begin(h, DFLASH_PROBE_ATTN, s);
+      h->launches += 2;
+      if ((st = dflash_cache_attention(h->cache, &ca, stream))) return st;
+      if (i == 0) probe_end(h, DFLASH_PROBE_ATTN, s);
+    } else {
       AttnArgs aa{};
       aa.q = h->q;
       aa.kb = h->kb;
@@ -1460,6 +1624,7 @@ int dflash_accept_kept(dflash_handle* h, int n_req, const int32_t* draft, const 
 
 int dflash_reset_request(dflash_handle* h, int req_id) {
   if (!h || req_id < 0 || req_id >= h->cfg.max_batch) return DFLASH_EINVAL;
+  if (h->ctx_len[req_id] > 0) h->reset_pending[req_id] = true;
   h->ctx_len[req_id] = 0;
   return DFLASH_OK;
 }
@@ -1482,9 +1647,10 @@ int dflash_check_errors(dflash_handle* h, void* stream) {
         cudaMemset(h->tickets, 0, (size_t)h->ticket_count * 4) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess)
       return DFLASH_ECUDA;
-    return (word & kErrBounds) ? DFLASH_EBOUNDS : DFLASH_ETIMEOUT;
+    const int paged = h->cache ? dflash_cache_check_errors(h->cache, stream) : DFLASH_OK;   // cleared too
+    return (word & kErrBounds) || paged == DFLASH_EBOUNDS ? DFLASH_EBOUNDS : DFLASH_ETIMEOUT;
   }
-  return DFLASH_OK;
+  return h->cache ? dflash_cache_check_errors(h->cache, stream) : DFLASH_OK;
 }
 
 int dflash_get_stats(const dflash_handle* h, dflash_stats* out) {
@@ -1520,6 +1686,13 @@ int dflash_set_wait_limit(dflash_handle* h, unsigned limit_us, void* stream) {
 int dflash_debug_stall(dflash_handle* h, int cta) {
   if (!h) return DFLASH_EINVAL;
   h->stall_armed = cta < 0 ? 0 : cta + 1;
+  return DFLASH_OK;
+}
+
+int dflash_ctx_cache(const dflash_handle* h, dflash_cache_config* cache, dflash_pool* pool) {
+  if (!h || !h->cache || !cache || !pool) return DFLASH_EINVAL;
+  *cache = h->cache_cfg;
+  *pool = h->pool;
   return DFLASH_OK;
 }
 
@@ -1589,7 +1762,10 @@ int dflash_rows_matmul(dflash_handle* h, int matrix, int layer, int n_rows, cons
   return status_of(launch_tc05(a, p, n_rows, m->n_rows, half, y, ldy, static_cast<cudaStream_t>(stream)));
 }
 
-void dflash_destroy(dflash_handle* h) { delete h; }
+void dflash_destroy(dflash_handle* h) {
+  if (h) dflash_cache_destroy(h->cache);
+  delete h;
+}
 
 const char* dflash_status_str(int s) {
   switch (s) {

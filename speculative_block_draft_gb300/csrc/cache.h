@@ -59,4 +59,13 @@ struct CacheAttnArgs {
 cudaError_t launch_cache_attn(int dtype, const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                               cudaStream_t s);
 
+// Host numbers into device arrays (a launch of their own, so they may be captured): d_req[i] = req[i], d_n[i] = n[i].
+struct PoolNumbers {
+  int n_req;
+  int32_t req[DFLASH_MAX_BATCH], n[DFLASH_MAX_BATCH];
+};
+cudaError_t launch_pool_numbers(const PoolNumbers& v, int32_t* d_req, int32_t* d_n, cudaStream_t s);
+// All blocks free: free_list = n_blocks - 1 .. 0 (taken from block 0 on), free_count = n_blocks.
+cudaError_t launch_pool_init(int n_blocks, int32_t* free_list, int32_t* free_count, cudaStream_t s);
+
 }  // namespace dfl

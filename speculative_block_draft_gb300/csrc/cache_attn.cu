@@ -1033,9 +1033,10 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
 constexpr int kJoinWarps = 8, kOwnTile = 16;           // own rows in shared memory at a time
 __host__ __device__ constexpr int join_rows(int hd) { return kJoinWarps * 256 / hd; }
 
-template <typename T, int HD>
+// kAtOnce: pieces in flight, eight where a row has many (a long context of few requests), else four for the occupancy.
+template <typename T, int HD, int kAtOnce>
 __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
-  constexpr int LPR = HD / 8, kAtOnce = 4;             // lanes of a row; pieces in flight
+  constexpr int LPR = HD / 8;                          // lanes of a row
   constexpr int kStep = LPR / 8;                       // lanes between the scores of neighbouring own rows
   constexpr int kLoads = kOwnTile * LPR / (kJoinWarps * 32) > 0 ? kOwnTile * LPR / (kJoinWarps * 32) : 1;
   __shared__ uint4 own[2][kOwnTile][LPR];              // K, V
@@ -1205,7 +1206,8 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtens
   e = launch_pdl(cache_attn_kernel<T, HD, RP>, dim3(a.grid), dim3(kThreads), a.p.smem, s, a, kmap, vmap);
   if (e != cudaSuccess) return e;
   const dim3 join_grid(a.n_req * a.n_kv * a.p.chunks, (a.p.rc + join_rows(HD) - 1) / join_rows(HD));
-  return launch_pdl(cache_attn_join_kernel<T, HD>, join_grid, dim3(kJoinWarps * 32), 0, s, a);
+  const bool many = a.grid >= 6 * (int)join_grid.x;    // pieces of a row: about the CTAs per (request, KV head, chunk)
+  return launch_pdl(many ? cache_attn_join_kernel<T, HD, 8> : cache_attn_join_kernel<T, HD, 4>, join_grid, dim3(kJoinWarps * 32), 0, s, a);
 }
 
 template <typename T, int HD>

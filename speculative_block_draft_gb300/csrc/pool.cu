@@ -201,6 +201,22 @@ __global__ void __launch_bounds__(kPoolThreads) pool_truncate_kernel(const __gri
   }
 }
 
+__global__ void __launch_bounds__(DFLASH_MAX_BATCH) pool_numbers_kernel(const __grid_constant__ PoolNumbers v, int32_t* d_req, int32_t* d_n) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int i = threadIdx.x;
+  if (i < v.n_req) {
+    d_req[i] = v.req[i];
+    if (d_n) d_n[i] = v.n[i];
+  }
+}
+
+__global__ void __launch_bounds__(256) pool_init_kernel(int n_blocks, int32_t* free_list, int32_t* free_count) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < n_blocks) free_list[i] = n_blocks - 1 - i;
+  if (i == 0) *free_count = n_blocks;
+}
+
 int log2_of(int x) {
   int l = 0;
   while ((1 << l) < x) l++;
@@ -214,6 +230,15 @@ bool pool_ok(const dflash_pool* p, int n_req) {
 }
 
 }  // namespace
+
+cudaError_t launch_pool_numbers(const PoolNumbers& v, int32_t* d_req, int32_t* d_n, cudaStream_t s) {
+  return launch_pdl(pool_numbers_kernel, dim3(1), dim3(DFLASH_MAX_BATCH), 0, s, v, d_req, d_n);
+}
+
+cudaError_t launch_pool_init(int n_blocks, int32_t* free_list, int32_t* free_count, cudaStream_t s) {
+  pool_init_kernel<<<(n_blocks + 255) / 256, 256, 0, s>>>(n_blocks, free_list, free_count);
+  return cudaGetLastError();
+}
 
 }  // namespace dfl
 

@@ -149,3 +149,19 @@ def test_reference_reserve_after_truncate_takes_the_same_blocks():
     assert (have, table, free[:count], count) == before
     _, again, *_ = ref.pool_reserve(T, False, have, table, free, count, [20, 1, 16, 0])
     assert again == slots
+
+
+def test_drafter_config_with_a_paged_cache(lib):
+    import dflash_synth as syn
+    nbytes = lambda cfg, **kw: lib.dflash_workspace_bytes(ctypes.byref(pkg.make_config(syn.with_overrides(cfg, **kw))))   # noqa: E731
+    c5 = syn.CONFIGS["c5"]
+    ring = nbytes(c5)
+    # 32 requests x 33 blocks of a 2048-token window, as the ring holds: half the bytes a row, and the join's workspace
+    paged = nbytes(c5, cache_blocks=32 * 33)
+    row = 5 * 2 * 8 * 128
+    assert ring > 0 and paged > 0
+    assert ring - nbytes(c5, cache_blocks=1) > 32 * 2048 * row * 2 - (64 << 20)
+    assert nbytes(c5, cache_blocks=2000) - nbytes(c5, cache_blocks=1000) == pytest.approx(1000 * (64 * row + 5 * 2 * 8 * 4 + 4), abs=4096)
+    assert nbytes(c5, cache_blocks=-1) == 0 and nbytes(c5, cache_blocks=1 << 25) == 0
+    assert nbytes(syn.CONFIGS["c1"], cache_blocks=8) == 0                    # fp32 drafter: the ring only
+    assert lib.dflash_ctx_cache(None, None, None) == pkg.DFLASH_EINVAL
