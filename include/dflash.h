@@ -362,7 +362,7 @@ typedef struct {
   int n_kv_heads, head_dim;  /* head_dim in {64, 128, 256} */
   int64_t layer_stride, block_stride, head_stride, token_stride;   /* bytes */
   /* limits of the attention calls (all 0: none are made) */
-  int n_q_heads;             /* a multiple of n_kv_heads */
+  int n_q_heads;             /* a multiple of n_kv_heads, at most 4096 times as many */
   int max_requests;          /* requests per call, <= DFLASH_CACHE_MAX_REQUESTS */
   int max_q;                 /* query rows per request, <= DFLASH_CACHE_MAX_Q */
 } dflash_cache_config;

@@ -27,7 +27,7 @@ def _debug_selected() -> bool:
     return os.environ.get("DFLASH_DEBUG_CHECKS") == "1"
 _SOURCES = ["abi.cu", "gemv_q4.cu", "gemv_bf16.cu", "gemv_f32.cu", "attn.cu", "misc.cu", "noalloc.cu", "gemm_tc05.cu", "tc05_epi.cu",
             "proj_tc05.cu", "pool.cu", "cache_append.cu", "cache_attn.cu", "cache_abi.cu"]
-_HEADERS = ["internal.h", "common.cuh", "gemv_impl.cuh", "gemm_tc05.h", "tc05.cuh", "cache.h"]
+_HEADERS = ["internal.h", "common.cuh", "gemv_impl.cuh", "gemm_tc05.h", "tc05.cuh", "cache.h", "tensor_map.h"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-gencode", "arch=compute_103a,code=sm_103a",
               "-Xcompiler", "-fPIC"]
 

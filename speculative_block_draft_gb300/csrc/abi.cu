@@ -12,6 +12,7 @@
 #include "gemm_tc05.h"
 #include "cache.h"
 #include "internal.h"
+#include "tensor_map.h"
 
 using namespace dfl;
 

@@ -41,6 +41,7 @@ CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req);
 struct CacheAttnArgs {
   const float *k_scale, *v_scale;                  // of the call's layer
   int layer, n_blocks, n_kv, hd, log_t, grp;
+  unsigned grp_mul;                                // 2^32 / grp, rounded up
   int n_req, n_rows, max_q, table_rows, table_blocks, causal, window;
   int held;                                        // tokens that a table row can name
   const int32_t *requests, *lens, *table, *row_start;

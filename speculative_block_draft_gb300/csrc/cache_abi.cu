@@ -6,6 +6,7 @@
 #include <new>
 
 #include "cache.h"
+#include "tensor_map.h"
 
 using namespace dfl;
 
@@ -44,7 +45,7 @@ bool valid(const dflash_cache_config* c) {
       c->token_stride >= (1LL << 40))
     return false;
   if (c->n_q_heads == 0 && c->max_requests == 0 && c->max_q == 0) return true;
-  return c->n_q_heads >= 1 && c->n_q_heads <= 65535 && c->n_q_heads % c->n_kv_heads == 0 && c->max_requests >= 1 &&
+  return c->n_q_heads >= 1 && c->n_q_heads % c->n_kv_heads == 0 && c->n_q_heads / c->n_kv_heads <= 4096 && c->max_requests >= 1 &&
          c->max_requests <= DFLASH_CACHE_MAX_REQUESTS && c->max_q >= 1 && c->max_q <= DFLASH_CACHE_MAX_Q;
 }
 
@@ -225,6 +226,7 @@ int dflash_cache_attention(dflash_cache* c, const dflash_attention* p, void* str
   a.hd = f.head_dim;
   a.log_t = c->log_t;
   a.grp = f.n_q_heads / f.n_kv_heads;
+  a.grp_mul = (unsigned)(((1ull << 32) + a.grp - 1) / a.grp);
   a.n_req = p->n_requests;
   a.n_rows = p->n_rows;
   a.max_q = p->max_q;

@@ -89,6 +89,9 @@ __device__ __forceinline__ void row_range(const CacheAttnArgs& a, const Request&
   hi = max(hi, 0);
 }
 
+// r / grp, for r < DFLASH_CACHE_MAX_Q * grp: by the rounded-up 2^32 / grp, exact while that times grp is below 2^32.
+__device__ __forceinline__ int by_group(const CacheAttnArgs& a, int r) { return a.grp == 1 ? r : (int)__umulhi((unsigned)r, a.grp_mul); }
+
 // What a call says about request b: first query row, query rows, cached tokens, table row.
 __device__ __forceinline__ int4 read_request(const CacheAttnArgs& a, int b) {
   int row0 = b * a.max_q, n = a.max_q;
@@ -377,7 +380,6 @@ struct alignas(16) RowState {            // per query row of the CTA's chunk
   float f[kRowArrays], by[kRowArrays];   // factor of a moved reference, minus its step; 1 / L at the end
   float red[4][kRowArrays];              // per softmax warp: maxima, sums
   uint32_t high[4];                      // per softmax warp: chunks of rows with a value above kMax
-  int lo[kRowArrays], hi[kRowArrays];    // visible positions
   int unset[kRowArrays];                 // the row has seen no key (its reference is 0)
   int64_t out[kRowArrays];               // its element offset in the output
 };
@@ -410,7 +412,7 @@ __device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Se
       const int r = first + u * at_once;
       v[u] = make_uint4(0, 0, 0, 0);
       if (r < rows) {
-        const int row = sg.r.row0 + (r0 + r) / a.grp, head = sg.head * a.grp + (r0 + r) % a.grp;
+        const int i = by_group(a, r0 + r), row = sg.r.row0 + i, head = sg.head * a.grp + r0 + r - i * a.grp;
         v[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + row * a.q_row + head * a.q_head + c8);
       }
     }
@@ -752,22 +754,17 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
       if (key < RP) {
         rs.neg_m[key] = 0.f;
         rs.unset[key] = key < rows;
-        int lo = 0, hi = 0;
-        if (key < rows) {
-          const int i = (r0 + key) / a.grp;
-          row_range(a, sg.r, i, lo, hi);
-          rs.out[key] = (sg.r.row0 + i) * a.o_row + (sg.head * a.grp + (r0 + key) - i * a.grp) * a.o_head;
-        }
-        rs.lo[key] = lo;
-        rs.hi[key] = hi;
+        const int i = by_group(a, r0 + key);
+        rs.out[key] = (sg.r.row0 + i) * a.o_row + (sg.head * a.grp + r0 + key - i * a.grp) * a.o_head;   // where key < rows
       }
       const float* row_qs = rs.qs[n_seg & 1];
       wait(n_seg == 0 ? q_first : &q_full[n_seg & 1], n_seg == 0 ? 0 : (n_seg - 1) >> 1);   // the query scales
       softmax_sync();
 
       int lo_all, hi_all, dummy;                       // keys that every row sees
-      row_range(a, sg.r, r0 / a.grp, dummy, hi_all);
-      row_range(a, sg.r, (r0 + rows - 1) / a.grp, lo_all, dummy);
+      row_range(a, sg.r, by_group(a, r0), dummy, hi_all);
+      row_range(a, sg.r, by_group(a, r0 + rows - 1), lo_all, dummy);
+      const int at0 = a.k_own ? sg.r.len : sg.r.len - sg.r.n;   // position of the request's first row
       bool unset_any = true;                           // some row has seen no key
       float2 l[CH * 4];
 #pragma unroll
@@ -790,17 +787,18 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
         uint32_t sees[2] = {~0u, ~0u};                   // rows 0-31, 32-63
         bool v_nan = false;
         if (!whole) {
-          sees[0] = sees[1] = 0;
-          if (seen)
-#pragma unroll 1
-            for (int r = 0; r < RP; r++) {
-              const uint32_t bit = (uint32_t)(pos >= rs.lo[r] && pos < rs.hi[r]) << (r & 31);
-              if (r < 32) sees[0] |= bit;
-              else sees[1] |= bit;
-            }
+          // row i of the request sees it from i = pos - at0 on, and with a window for so many rows
+          uint64_t bits = 0;
+          if (seen) {
+            const int i0 = a.causal ? min(max(pos - at0, 0), sg.r.n) : 0;
+            const int i1 = a.causal && a.window > 0 ? (int)min((long long)pos - at0 + a.window, (long long)sg.r.n) : sg.r.n;
+            const int ra = min(max(i0 * a.grp - r0, 0), RP), rb = min(max(i1 * a.grp - r0, ra), RP);
+            bits = (rb == 64 ? ~0ull : (1ull << rb) - 1) & ~(ra == 64 ? ~0ull : (1ull << ra) - 1);
+          }
+          sees[0] = (uint32_t)bits, sees[1] = (uint32_t)(bits >> 32);
           const int sq = base + (t + 1 < n_tiles ? 2 * t + 2 : 2 * n_tiles - 1), slot = sq % S;
           if (!wait_bar(&full[slot], sq / S, a.err)) dead[look & 1] = 1;
-#pragma unroll 1
+#pragma unroll 4
           for (int c = 0; c < HD / 16; c++) {
             uint4* at = reinterpret_cast<uint4*>(ring + (size_t)slot * STAGE + (c >> 3) * PANEL + key * ROWB + (c & 7) * 16);
             uint4 w = make_uint4(0, 0, 0, 0), bad = w;
@@ -1001,12 +999,16 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
             for (int j = 0; j < 8; j++) o8[j] = i == 0 ? __uint_as_float(part8[i][j]) : o8[j] + __uint_as_float(part8[i][j]);
           }
           if (key < HD) {
+            const int left = rows - ch;
+            if (direct) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-              if (ch + j < rows) {
-                if (direct) row_store(out + rs.out[ch + j] + p * 128, o8[j] * rs.f[ch + j]);
-                else part[(ch + j) * HD + p * 128] = o8[j];
-              }
+              for (int j = 0; j < 8; j++)
+                if (j < left) row_store(out + rs.out[ch + j] + p * 128, o8[j] * rs.f[ch + j]);
+            } else {
+              float* to = part + ch * HD + p * 128;
+#pragma unroll
+              for (int j = 0; j < 8; j++)
+                if (j < left) to[j * HD] = o8[j];
             }
           }
         }
@@ -1059,7 +1061,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
   }
   const int r = min(r_cta + warp * (32 / LPR) + lane / LPR, rows - 1);    // spare lanes repeat the last row
   const bool live = r == r_cta + warp * (32 / LPR) + lane / LPR;
-  const int rr = chunk * a.p.rc + r, i = rr / a.grp, qh = head * a.grp + rr - i * a.grp, row = rq.row0 + i;
+  const int rr = chunk * a.p.rc + r, i = by_group(a, rr), qh = head * a.grp + rr - i * a.grp, row = rq.row0 + i;
   const int n_own = a.k_own ? rq.n : 0;
   // own rows of a tile: this thread's pieces on their way, then into shared memory
   uint4 kw[kLoads], vw[kLoads];

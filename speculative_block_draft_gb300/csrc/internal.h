@@ -214,27 +214,6 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   return launch_pdl_cluster(kernel, grid, block, smem, s, 1, std::forward<Args>(args)...);
 }
 
-// The driver's tensor-map encoder, looked up once per process.
-typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-inline EncodeTiled tensor_map_encoder() {
-  static std::atomic<EncodeTiled> encode{nullptr};
-  EncodeTiled e = encode.load(std::memory_order_acquire);
-  if (!e) {
-    cudaDriverEntryPointQueryResult q;
-    void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !fn)
-      return nullptr;
-    e = reinterpret_cast<EncodeTiled>(fn);
-    encode.store(e, std::memory_order_release);
-  }
-  return e;
-}
-
 // ---- launchers (return cudaGetLastError of the launch) -----------------------------------------
 cudaError_t launch_gemv(int fmt, int epi, int nt, const GemvArgs& a, int grid, cudaStream_t s);
 // Final greedy token + confidence per row from n_parts (max, sum, index) states kMaxRows rows apart;

@@ -162,18 +162,19 @@ __global__ void __launch_bounds__(kPoolThreads) pool_reserve_kernel(const __grid
 __global__ void __launch_bounds__(kPoolThreads) pool_truncate_kernel(const __grid_constant__ PoolArgs a) {
   __shared__ int sums[32];
   __shared__ int rows[kPoolThreads], from[kPoolThreads], start[kPoolThreads + 1];
+  __shared__ bool last;
   const int i = threadIdx.x;
   pdl_launch_dependents();
   pdl_wait();
   const int r = request_row(a, rows);
   const int count = min(max(*a.p.free_count, 0), a.p.n_blocks);
-  int after = 0, gone = 0;
+  int after = 0, gone = 0, keep = -1;
   if (r >= 0) {
-    const int len = a.p.lens[r], keep = a.n[i];
-    if (len > 0 && keep >= 0 && keep < len) {
+    const int len = a.p.lens[r], n = a.n[i];
+    if (len > 0 && n >= 0 && n < len) {
+      keep = n;
       after = blocks_of(keep, a);
       gone = max(0, min(blocks_of(len, a), a.p.table_blocks) - after);
-      a.p.lens[r] = keep;
     }
   }
   int total;
@@ -182,12 +183,19 @@ __global__ void __launch_bounds__(kPoolThreads) pool_truncate_kernel(const __gri
   rows[i] = r;
   from[i] = after;
   start[i] = end - gone;
-  if (i == 0) {
-    start[kPoolThreads] = total;
-    *a.p.free_count = min(count + total, a.p.n_blocks);
-  }
+  if (i == 0) start[kPoolThreads] = total;
   __syncthreads();
-  for (int g = i; g < total; g += kPoolThreads) {
+  // as in the reservation, the last CTA to have read the lengths and the count writes the new ones
+  if (i == 0) last = gridDim.x == 1 || atom_add_acq_rel_gpu(static_cast<int*>(a.p.scratch), 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (last) {
+    if (keep >= 0) a.p.lens[r] = keep;
+    if (i == 0) {
+      *a.p.free_count = min(count + total, a.p.n_blocks);
+      *static_cast<int*>(a.p.scratch) = 0;
+    }
+  }
+  for (int g = blockIdx.x * kPoolThreads + i; g < total; g += gridDim.x * kPoolThreads) {
     int lo = 0, hi = kPoolThreads;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -280,7 +288,9 @@ extern "C" int dflash_pool_truncate(const dflash_pool* p, int n_requests, const 
   a.log_t = log2_of(p->block_tokens);
   a.requests = requests;
   a.n = new_len;
-  return launch_pdl(pool_truncate_kernel, dim3(1), dim3(kPoolThreads), 0, static_cast<cudaStream_t>(stream), a) ==
+  // a CTA for every 4096 table entries that might be released
+  const int grid = (int)std::min<int64_t>(32, std::max<int64_t>(1, (int64_t)n_requests * p->table_blocks / (4 * kPoolThreads)));
+  return launch_pdl(pool_truncate_kernel, dim3(grid), dim3(kPoolThreads), 0, static_cast<cudaStream_t>(stream), a) ==
                  cudaSuccess
              ? DFLASH_OK
              : DFLASH_ECUDA;
