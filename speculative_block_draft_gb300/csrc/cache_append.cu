@@ -8,11 +8,14 @@
 // power of two loses nothing against amax / 448, and when it grows, the codes that stay move by
 // whole exponents (only those that become subnormal are rounded again).
 //
-// A run is the rows of one block. Two kernels, by the rows of a call:
-//  * few rows (rounds: short runs): one warp per (run, head and side, layer), latency-bound. Every row has a
-//    warp; 32 slots in one load tell it whether a run starts there and where it ends.
-//  * many rows (prompts: whole blocks): one CTA per (run, head and side, layer), HBM-bound. A block's rows
-//    stay in registers between the amax and the rounding, so they are read once.
+// A run is the rows of one block. A CTA takes the runs that start among some rows, for some heads of one side and
+// layer, each in one of two ways by its length:
+//  * long (prompts: whole blocks): its 256 threads together, HBM-bound; the rows stay in registers between the
+//    amax and the rounding, so they are read once, and the next head's are on their way meanwhile;
+//  * at most kShortRun rows (rounds): a warp per run and head, latency-bound.
+// Measured, 5 layers x 8 heads x 128 columns of bf16: 128 rows in 2 runs 4.4 us together, 16.5 us by warps; 512
+// rows in 64 runs 33.9 us together, 7.0 us by warps. 16384 rows: 97 us, 5.2 TB/s read and written (the floor at the
+// measured copy bandwidth is 74 us).
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -26,7 +29,7 @@ namespace dfl {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kFewRows = 2048;     // up to here a warp per run, above a CTA
+constexpr int kShortRun = 16;
 
 // 8 consecutive elements of a row: fetched as they are, read as fp32.
 template <typename T>
@@ -179,125 +182,118 @@ __device__ __forceinline__ void regrade8(uint2* at, float ratio) {
   *at = to_codes(x);
 }
 
-constexpr int kWarpUnits = 8;      // warps per CTA of the few-rows kernel: heads and sides of one row
-constexpr int kHeld = 4;           // eighths of a row that a lane of it holds at once
+constexpr int kHeld = 4;           // eighths of a row that a lane holds at once
 
+// The run that starts at `row`, by one warp; owner: block_tokens words of shared memory of its own.
 template <typename T>
-__global__ void __launch_bounds__(kWarpUnits * 32) cache_append_few_kernel(const __grid_constant__ CacheAppendArgs a) {
-  __shared__ int owners[kWarpUnits][128];   // last row of the call for each token of the block, -1: none
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int unit = blockIdx.y * kWarpUnits + warp;
-  const int head = unit >> 1, side = unit & 1, layer = a.layer0 + blockIdx.z;
-  const int n_tok = 1 << a.log_t;
-  int* owner = owners[warp];
-  pdl_launch_dependents();
-  pdl_wait();
-  if (head >= a.n_kv) return;
-  for (int row = blockIdx.x * a.rows_per_cta; row < min(a.n_rows, (int)(blockIdx.x + 1) * a.rows_per_cta); row++) {
-    // lane l: the row l - 1 further on
-    auto block_of = [&](int r) { return r >= 0 && r < a.n_rows ? block_at(a, r) : -1; };
-    int b = block_of(row - 1 + lane);
-    const int block = __shfl_sync(0xffffffffu, b, 1), prev = __shfl_sync(0xffffffffu, b, 0);
-    if (block < 0 || prev == block || (row > 0 && prev < 0 && !starts_run(a, row, block))) continue;
-    Target to(a, layer, block, head, side);
-    for (int t = lane; t < n_tok; t += 32) owner[t] = -1;
-    __syncwarp();
-    // its rows: up to the first one of another block
-    int end = row;
-    for (int r0 = row - 1;; r0 += 32) {
-      if (r0 >= row) b = block_of(r0 + lane);
-      const bool mine = r0 + lane >= row;
-      const unsigned other = __ballot_sync(0xffffffffu, mine && b >= 0 && b != block);
-      const int stop = other ? __ffs(other) - 1 : 32;
-      if (mine && lane < stop && b == block) atomicMax(&owner[a.slots[r0 + lane] & (n_tok - 1)], r0 + lane);
-      end = r0 + stop;
-      if (other || end >= a.n_rows) break;
-    }
-    end = min(end, a.n_rows);
-    __syncwarp();
-    const T* src = static_cast<const T*>(a.rows[side]) + blockIdx.z * a.row_layer[side] + head * a.row_head[side];
-    const int per_row = a.hd / 8, at_once = 32 / per_row, c8 = (lane % per_row) * 8;
-    // kHeld rows of this lane's group of lanes at a time, all their loads in flight; a short run is read once
-    Row8<T> x[kHeld];
-    int tok[kHeld];
-    auto fetch = [&](int r0) {
+__device__ __forceinline__ void append_by_warp(const CacheAppendArgs& a, int row, int layer, int head, int side, int* owner) {
+  const int lane = threadIdx.x & 31, n_tok = 1 << a.log_t, block = block_at(a, row);
+  Target to(a, layer, block, head, side);
+  for (int t = lane; t < n_tok; t += 32) owner[t] = -1;
+  __syncwarp();
+  // its rows: up to the first one of another block
+  int end = row;
+  for (int r0 = row;; r0 += 32) {
+    const int b = r0 + lane < a.n_rows ? block_at(a, r0 + lane) : -1;
+    const unsigned other = __ballot_sync(0xffffffffu, b >= 0 && b != block);
+    const int stop = other ? __ffs(other) - 1 : 32;
+    if (lane < stop && b == block) atomicMax(&owner[a.slots[r0 + lane] & (n_tok - 1)], r0 + lane);
+    end = r0 + stop;
+    if (other || end >= a.n_rows) break;
+  }
+  end = min(end, a.n_rows);
+  __syncwarp();
+  const T* src = static_cast<const T*>(a.rows[side]) + (layer - a.layer0) * a.row_layer[side] + head * a.row_head[side];
+  const int per_row = a.hd / 8, at_once = 32 / per_row, c8 = (lane % per_row) * 8;
+  // kHeld rows of this lane's group of lanes at a time, all their loads in flight; a short run is read once
+  Row8<T> x[kHeld];
+  int tok[kHeld];
+  auto fetch = [&](int r0) {
 #pragma unroll
-      for (int i = 0; i < kHeld; i++) {
-        const int r = r0 + i * at_once, s = r < end ? a.slots[r] : -1;
-        tok[i] = s >= 0 && owner[s & (n_tok - 1)] == r ? s & (n_tok - 1) : -1;
-        if (tok[i] >= 0) x[i].fetch(src + r * a.row_row[side] + c8);
-      }
-    };
-    float v[8];
-    uint32_t top = 0;
-    const int step = kHeld * at_once;
+    for (int i = 0; i < kHeld; i++) {
+      const int r = r0 + i * at_once, s = r < end ? a.slots[r] : -1;
+      tok[i] = s >= 0 && owner[s & (n_tok - 1)] == r ? s & (n_tok - 1) : -1;
+      if (tok[i] >= 0) x[i].fetch(src + r * a.row_row[side] + c8);
+    }
+  };
+  float v[8];
+  uint32_t top = 0;
+  const int step = kHeld * at_once;
+  for (int r0 = row; r0 < end; r0 += step) {
+    fetch(r0 + lane / per_row);
+#pragma unroll
+    for (int i = 0; i < kHeld; i++)
+      if (tok[i] >= 0) top = x[i].top(top);
+  }
+  top = Row8<T>::warp_top(top);
+  float amax = Row8<T>::value(top);
+  if (!Row8<T>::finite(top)) {
+    amax = 0.f;
     for (int r0 = row; r0 < end; r0 += step) {
       fetch(r0 + lane / per_row);
 #pragma unroll
       for (int i = 0; i < kHeld; i++)
-        if (tok[i] >= 0) top = x[i].top(top);
+        if (tok[i] >= 0) amax = x[i].finite_amax(amax);
     }
-    top = Row8<T>::warp_top(top);
-    float amax = Row8<T>::value(top);
-    if (!Row8<T>::finite(top)) {
-      amax = 0.f;
-      for (int r0 = row; r0 < end; r0 += step) {
-        fetch(r0 + lane / per_row);
-#pragma unroll
-        for (int i = 0; i < kHeld; i++)
-          if (tok[i] >= 0) amax = x[i].finite_amax(amax);
-      }
-      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-    }
-    to.settle(amax, owner[0] >= 0);
-    const Divide div(to.now);
-    for (int r0 = row; r0 < end; r0 += step) {
-      if (end - row > step) fetch(r0 + lane / per_row);
-#pragma unroll
-      for (int i = 0; i < kHeld; i++)
-        if (tok[i] >= 0) {
-          x[i].get(v);
-          *reinterpret_cast<uint2*>(to.codes + tok[i] * a.c_token + c8) = div.codes(v);
-        }
-    }
-    if (to.regrade) {
-      const float ratio = __fdiv_rn(to.old, to.now);
-      for (int t = lane / per_row; t < n_tok; t += at_once)
-        if (owner[t] < 0) regrade8(reinterpret_cast<uint2*>(to.codes + t * a.c_token + c8), ratio);
-    }
-    if (lane == 0) *to.scale = to.now;
-    __syncwarp();   // owner belongs to the next run
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
   }
+  to.settle(amax, owner[0] >= 0);
+  const Divide div(to.now);
+  for (int r0 = row; r0 < end; r0 += step) {
+    if (end - row > step) fetch(r0 + lane / per_row);
+#pragma unroll
+    for (int i = 0; i < kHeld; i++)
+      if (tok[i] >= 0) {
+        x[i].get(v);
+        *reinterpret_cast<uint2*>(to.codes + tok[i] * a.c_token + c8) = div.codes(v);
+      }
+  }
+  if (to.regrade) {
+    const float ratio = __fdiv_rn(to.old, to.now);
+    for (int t = lane / per_row; t < n_tok; t += at_once)
+      if (owner[t] < 0) regrade8(reinterpret_cast<uint2*>(to.codes + t * a.c_token + c8), ratio);
+  }
+  if (lane == 0) *to.scale = to.now;
+  __syncwarp();   // owner belongs to the next run
 }
 
-// PER: eighths of a row per thread, block_tokens * head_dim / 8 / 256 (at least 1). A CTA takes the runs that
-// start among its block_tokens rows (a prompt has one), for `heads` heads of one side and layer: the rows of the
-// next head are on their way while one head's are rounded.
+// PER: eighths of a row per thread, block_tokens * head_dim / 8 / 256 (at least 1).
 template <typename T, int PER>
 __global__ void __launch_bounds__(kAppendThreads, PER * sizeof(T) <= 8 ? 4 : 1)
     cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
-  __shared__ int owner[128];       // last row of the call for each token of the block, -1: none
+  __shared__ int owners[kAppendThreads / 32][128];   // last row of the call for each token of the block, -1: none
+  int* owner = owners[0];
   __shared__ uint32_t wtop[2][kAppendThreads / 32];
-  __shared__ int starts[128], n_starts, run_end;
+  __shared__ int starts[2][128], n_starts[2], run_end;   // first rows of the short and of the long runs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int side = blockIdx.y & 1, head0 = (blockIdx.y >> 1) * a.heads, head1 = min(a.n_kv, head0 + a.heads);
   const int layer = a.layer0 + blockIdx.z, n_tok = 1 << a.log_t, per_row = a.hd / 8;
-  if (tid == 0) n_starts = 0;
+  if (tid < 2) n_starts[tid] = 0;
   pdl_launch_dependents();
   pdl_wait();
   __syncthreads();
   {
-    const int row = (blockIdx.x << a.log_t) + tid;
-    if (tid < n_tok && row < a.n_rows) {
+    const int row = blockIdx.x * a.rows_per_cta + tid;
+    if (tid < a.rows_per_cta && row < a.n_rows) {
       const int b = block_at(a, row);
-      if (b >= 0 && starts_run(a, row, b)) starts[atomicAdd(&n_starts, 1)] = row;
+      if (b >= 0 && starts_run(a, row, b)) {
+        const int is_long = row + kShortRun < a.n_rows && block_at(a, row + kShortRun) == b;
+        starts[is_long][atomicAdd(&n_starts[is_long], 1)] = row;
+      }
     }
   }
   __syncthreads();
-  const int runs = n_starts;
+  {
+    const int runs = n_starts[0], tasks = runs * (head1 - head0);
+    for (int u = warp; u < tasks; u += kAppendThreads / 32)
+      append_by_warp<T>(a, starts[0][u % runs], layer, head0 + u / runs, side, owners[warp]);
+  }
+  if (n_starts[1] == 0) return;
+  __syncthreads();                 // owners
+  const int runs = n_starts[1];
   const T* src = static_cast<const T*>(a.rows[side]) + blockIdx.z * a.row_layer[side];
   for (int u = 0; u < runs; u++) {
-    const int row = starts[u], block = block_at(a, row);
+    const int row = starts[1][u], block = block_at(a, row);
     for (int t = tid; t < n_tok; t += kAppendThreads) owner[t] = -1;
     if (tid == 0) run_end = a.n_rows;
     __syncthreads();
@@ -378,17 +374,18 @@ __global__ void __launch_bounds__(kAppendThreads, PER * sizeof(T) <= 8 ? 4 : 1)
 
 template <typename T>
 cudaError_t launch_rows(CacheAppendArgs a, cudaStream_t s) {
-  // heads per CTA: as many as leave several CTAs for every SM
-  const long long blocks = ((a.n_rows + (1 << a.log_t) - 1) >> a.log_t) * 2LL * a.n_layers;
+  // Heads per CTA: as many as leave several CTAs for every SM; with more, a CTA has loads on their way while it rounds.
+  // Rows per CTA: as few (8 to 64, or a block's) as give about one wave of CTAs, four per SM, so that the runs of a
+  // round spread: 144 rows in 32 runs take 7.4 us with 64 rows per CTA and 4.8 us with 16, 512 rows in 64 runs 6.9 and
+  // 11.9 us (5 layers x 8 heads).
+  const long long blocks = (a.n_rows + (1 << a.log_t) - 1) >> a.log_t;
   a.heads = a.n_kv;
-  while (a.heads > 1 && blocks * ((a.n_kv + a.heads - 1) / a.heads) < 2048) a.heads = (a.heads + 1) / 2;
-  const unsigned layers = a.n_layers;
-  // a row per CTA, or as many as leave about three CTAs for every SM: most rows start no run
-  const int units = (2 * a.n_kv + kWarpUnits - 1) / kWarpUnits;
-  a.rows_per_cta = (int)std::max(1LL, std::min(8LL, (long long)a.n_rows * units * a.n_layers / 456));
-  if (a.n_rows <= kFewRows)
-    return launch_pdl(cache_append_few_kernel<T>, dim3((a.n_rows + a.rows_per_cta - 1) / a.rows_per_cta, units, layers), dim3(kWarpUnits * 32), 0, s, a);
-  const dim3 grid((a.n_rows + (1 << a.log_t) - 1) >> a.log_t, 2 * ((a.n_kv + a.heads - 1) / a.heads), layers), block(kAppendThreads);
+  while (a.heads > 1 && blocks * 2 * a.n_layers * ((a.n_kv + a.heads - 1) / a.heads) < 2048) a.heads = (a.heads + 1) / 2;
+  const long long per_row = 2LL * a.n_layers * ((a.n_kv + a.heads - 1) / a.heads);
+  a.rows_per_cta = 8;
+  while (a.rows_per_cta < std::max(64, 1 << a.log_t) && per_row * a.n_rows > 608LL * a.rows_per_cta) a.rows_per_cta *= 2;
+  const long long row_ctas = (a.n_rows + a.rows_per_cta - 1) / a.rows_per_cta;
+  const dim3 grid((unsigned)row_ctas, 2 * ((a.n_kv + a.heads - 1) / a.heads), a.n_layers), block(kAppendThreads);
   switch (((a.hd / 8) << a.log_t) / kAppendThreads) {
     case 0: case 1: return launch_pdl(cache_append_kernel<T, 1>, grid, block, 0, s, a);
     case 2: return launch_pdl(cache_append_kernel<T, 2>, grid, block, 0, s, a);
