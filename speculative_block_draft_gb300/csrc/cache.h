@@ -34,6 +34,7 @@ struct CacheAttnPlan {
   int chunks, rc, rp;
   int ns, n;               // MMA columns: rp, and terms * rp, rounded up to 16 (n <= 128)
   int ctas_per_sm, stages, tmem_cols;
+  int setup;               // tiles that the start and end of a chunk count for when the work is shared out
   size_t smem;
 };
 CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req);
@@ -52,7 +53,8 @@ struct CacheAttnArgs {
   unsigned* err;
   CacheAttnPlan p;
   int grid;                                        // CTAs of the first kernel
-  int* units;                                      // [n_req + 1] key tiles before each request
+  int4* words;                                     // [n_req] what the call says about each request (read_request)
+  int* units;                                      // [n_req + 1] units before each request, and those of a setup
   float* part_o;                                   // [grid + n_req * n_kv * chunks][rp][hd]
   float2* part_ml;                                 // [..][rp] (reference, sum)
 };

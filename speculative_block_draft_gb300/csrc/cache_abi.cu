@@ -15,7 +15,7 @@ struct dflash_cache {
   int device = 0, log_t = 0;
   unsigned* err = nullptr;      // [0] error bits, [1] wait limit in us (0: 1 s)
   int n_sm = 148;
-  int* units = nullptr;         // [max_requests + 1]
+  int4* requests = nullptr;     // [max_requests], then units: [max_requests + 2] ints
   float2* part_ml = nullptr;    // attention pieces: rows of (reference, sum), then of head_dim floats
   float* part_o = nullptr;
   int64_t part_rows = 0;
@@ -50,24 +50,24 @@ bool valid(const dflash_cache_config* c) {
 }
 
 // Rows of attention pieces that a call within the limits can leave: one per query row, padded, of each
-// (request, KV head), and the CTAs' own. A chunk of rows is padded by at most 23 (41 rows as 64) and a share of one
+// (request, KV head), and the CTAs' own. A chunk of rows is padded by at most 15 (49 rows as 64) and a share of one
 // row, and there is one for every 40 rows at most; a CTA's chunk holds at most 64 rows, and an SM two CTAs.
 int64_t piece_rows(const dflash_cache_config& f, int n_sm) {
   const int64_t rows = (int64_t)(f.n_q_heads / f.n_kv_heads) * f.max_q;
-  return (int64_t)2 * n_sm * 64 + (int64_t)f.max_requests * f.n_kv_heads * (rows + 24 * ((rows + 39) / 40));
+  return (int64_t)2 * n_sm * 64 + (int64_t)f.max_requests * f.n_kv_heads * (rows + 16 * ((rows + 39) / 40));
 }
 
 size_t round_256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// Workspace: error word | units | (m, L) of the pieces | O of the pieces.
+// Workspace: error word | requests and units | (m, L) of the pieces | O of the pieces.
 size_t carve(dflash_cache* c, uint8_t* base) {
   const dflash_cache_config& f = c->cfg;
   size_t at = 256;
   c->err = reinterpret_cast<unsigned*>(base);
   if (f.max_requests) {
     c->part_rows = piece_rows(f, c->n_sm);
-    c->units = reinterpret_cast<int*>(base + at);
-    at += round_256(4 * (size_t)(f.max_requests + 1));
+    c->requests = reinterpret_cast<int4*>(base + at);
+    at += round_256(16 * (size_t)f.max_requests + 4 * (size_t)(f.max_requests + 2));
     c->part_ml = reinterpret_cast<float2*>(base + at);
     at += round_256(8 * (size_t)c->part_rows);
     c->part_o = reinterpret_cast<float*>(base + at);
@@ -257,10 +257,11 @@ int dflash_cache_attention(dflash_cache* c, const dflash_attention* p, void* str
   // key tiles are counted in 32 bits: a request has at most as many as its table row names, and one more
   const int64_t pairs = (int64_t)p->n_requests * f.n_kv_heads * a.p.chunks;
   const int64_t tiles = pairs * ((((int64_t)p->table_blocks << c->log_t) + 127) / 128 + 1);
-  if (tiles >= (1LL << 31)) return DFLASH_EINVAL;
+  if (tiles + pairs * a.p.setup >= (1LL << 31)) return DFLASH_EINVAL;
   a.grid = (int)std::min<int64_t>((int64_t)a.p.ctas_per_sm * c->n_sm, tiles);
   if ((a.grid + pairs) * a.p.rp > c->part_rows) return DFLASH_ECAPACITY;
-  a.units = c->units;
+  a.words = c->requests;
+  a.units = reinterpret_cast<int*>(c->requests + f.max_requests);
   a.part_o = c->part_o;
   a.part_ml = c->part_ml;
   return status_of(launch_cache_attn(p->dtype, a, c->kmap, c->vmap, static_cast<cudaStream_t>(stream)));

@@ -52,7 +52,10 @@ constexpr int kMaxStages = 12;
 constexpr int kPBytes = kTile * 128;     // probabilities: 128 keys x up to 128 columns
 constexpr float kTop = 5.f, kMax = 8.75f;
 constexpr float kUnset = -1e30f;         // reference of a piece whose row has seen no key
-constexpr int kRowsOfTwo = 40;           // most rows with two CTAs per SM (registers)
+// Built for two CTAs per SM, with 128 registers per thread: 16 requests x 9 rows of 5 query heads, 128 columns, 71 us
+// with two CTAs and 90 us with one. With 256 columns shared memory holds one, and more registers help from 48 rows on
+// (66 us against 72; 24 rows 29.4 against 27.8).
+__host__ __device__ constexpr bool two_per_sm(int hd, int rp) { return rp <= (hd == 256 ? 40 : 48); }
 constexpr int kRowArrays = 64;           // rows of the per-row arrays in shared memory
 
 __device__ __forceinline__ float row_f(__half v) { return __half2float(v); }
@@ -120,7 +123,9 @@ __device__ __forceinline__ Request request_of(const CacheAttnArgs& a, int4 w) {
   return r;
 }
 
-// A CTA's run of units (key tiles) is units [first, last) of all; CTA c of g gets an equal share.
+// A CTA's run is units [first, last) of all; CTA c of g gets an equal share. A (request, KV head, row chunk) is
+// `setup` units, which stand for its queries, its first references and its output, then its key tiles. They count
+// nothing where there is a CTA for every tile.
 __device__ __forceinline__ long long unit_begin(int c, int total, int g) { return (long long)c * total / g; }
 
 // The tiles of one (request, KV head, row chunk) that a CTA's run holds.
@@ -148,14 +153,16 @@ struct Walk {
     while (u >= before[b + 1]) b++;
     s.b = b;
     s.r = request_of(a, words[b]);
-    const unsigned rem = u - before[b], tiles = s.r.tiles, chunks = s.r.chunks, p = rem / tiles;
+    const int setup = before[a.n_req + 1];
+    const unsigned rem = u - before[b], units = s.r.tiles + setup, chunks = s.r.chunks, p = rem / units;
+    const int at = rem - p * units, n = min((int)units - at, u_end - u);
     s.head = p / chunks;
     s.chunk = p - s.head * chunks;
     s.pair = (b * a.n_kv + s.head) * a.p.chunks + s.chunk;
-    s.t0 = rem - p * tiles;
-    s.t1 = min(s.r.tiles, s.t0 + (u_end - u));
-    u += s.t1 - s.t0;
-    return true;
+    s.t0 = max(at - setup, 0);
+    s.t1 = at + n - setup;
+    u += n;
+    return s.t1 > s.t0;                                // false only at the run's end
   }
 };
 
@@ -391,7 +398,7 @@ __host__ __device__ constexpr int panels_of(int hd) { return hd == 256 ? 2 : 1; 
 __host__ __device__ constexpr int stage_bytes(int hd) { return kTile * hd; }
 
 __host__ __device__ inline size_t attn_fixed_smem(int hd, int n, int n_req) {
-  return (size_t)2 * n * 128 * panels_of(hd) + kPBytes + sizeof(RowState) + (2 * kMaxStages + 12) * 8 + 64 + 20 * (size_t)(n_req + 1);
+  return (size_t)2 * n * 128 * panels_of(hd) + kPBytes + sizeof(RowState) + (2 * kMaxStages + 12) * 8 + 80 + 20 * (size_t)(n_req + 1);
 }
 
 // ---- the first kernel ----------------------------------------------------------------------------------
@@ -455,7 +462,7 @@ __device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Se
 // RP: query rows of a chunk, padded. It is known here so that the loops over the rows have no branches: with one, every
 // eight rows would wait for their own loads.
 template <typename T, int HD, int RP>
-__global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
     cache_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
   constexpr int TERMS = __is_same(T, __nv_bfloat16) ? 2 : 3;
@@ -479,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
   // Set when a softmax wait gave up, by turns for the stretches between two points where all softmax threads look
   // (just behind a barrier), so that all of them see the same and leave together
   volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* scan = reinterpret_cast<int*>(tmem_slot + 3);   // warp sums
-  int4* words = reinterpret_cast<int4*>(tmem_slot + 16);
+  uint64_t* scan = reinterpret_cast<uint64_t*>(tmem_slot + 4);   // warp sums
+  int4* words = reinterpret_cast<int4*>(tmem_slot + 20);
   int* before = reinterpret_cast<int*>(words + a.n_req);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -514,43 +521,55 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
   // this kernel, which would wait for it.
   pdl_launch_dependents();
   pdl_wait();
-  // key tiles before each request: one prefix sum over the requests, a few of them per thread
+  // units before each request: one prefix sum over the requests, a few of them per thread, of the key tiles (low half)
+  // and the setups (high half)
   {
     const int per = (a.n_req + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
-    int mine = 0;
+    auto work = [&](int b) -> uint64_t {
+      const Request r = request_of(a, words[b]);
+      const unsigned pairs = r.tiles > 0 ? r.chunks * a.n_kv : 0;
+      return (uint64_t)pairs << 32 | pairs * r.tiles;
+    };
+    uint64_t mine = 0;
 #pragma unroll 1
     for (int j = 0; j < per; j++)
       if (b0 + j < a.n_req) {
         words[b0 + j] = read_request(a, b0 + j);
-        const Request r = request_of(a, words[b0 + j]);
-        const int u = r.tiles * r.chunks * a.n_kv;
-        before[b0 + j] = u;
-        mine += u;
+        mine += work(b0 + j);
       }
-    int s = mine;
+    uint64_t s = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, s, o);
+      const uint64_t v = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += v;
     }
     if (lane == 31) scan[warp] = s;
     __syncthreads();
-    int at = s - mine;
+    uint64_t at = s - mine, all = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; w++) at += w < warp ? scan[w] : 0;
+    for (int w = 0; w < kThreads / 32; w++) {
+      at += w < warp ? scan[w] : 0;
+      all += scan[w];
+    }
+    const int setup = (uint32_t)all > (uint32_t)a.grid ? a.p.setup : 0;
 #pragma unroll 1
     for (int j = 0; j < per; j++)
       if (b0 + j < a.n_req) {
-        const int u = before[b0 + j];
-        before[b0 + j] = at;
-        at += u;
-        if (b0 + j == a.n_req - 1) before[a.n_req] = at;
+        before[b0 + j] = (int)((uint32_t)at + setup * (uint32_t)(at >> 32));
+        at += per > 1 ? work(b0 + j) : mine;
       }
+    if (threadIdx.x == 0) {
+      before[a.n_req] = (int)((uint32_t)all + setup * (uint32_t)(all >> 32));
+      before[a.n_req + 1] = setup;
+    }
   }
   __syncthreads();
   const int total = before[a.n_req], ctas = min(a.grid, total);
   if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b <= a.n_req; b += kThreads) a.units[b] = before[b];
+    for (int b = threadIdx.x; b <= a.n_req + 1; b += kThreads) {   // for the second kernel
+      if (b < a.n_req) a.words[b] = words[b];
+      a.units[b] = before[b];
+    }
   Walk walk{0, 0, 0};
   if ((int)blockIdx.x < ctas) {
     walk.u = (int)unit_begin(blockIdx.x, total, ctas);
@@ -567,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
   const uint32_t tmem_o = tmem + 2 * NS;
   Segment sg;
 
-  constexpr bool kSplitRegs = RP > 8 && RP <= kRowsOfTwo;
+  constexpr bool kSplitRegs = RP > 8 && two_per_sm(HD, RP);
   // queries of the first segment: all warps but the copy warp, which starts on the keys
   if (warp > 0) {
     Walk w = walk;
@@ -577,152 +596,152 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
     if (lane == 0) mbar_arrive(smem_u32(q_first));
   }
   if (warp < 4) {
-  if (kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == 0) {
-    // ---- copies: one per block of the tile (and 128-byte panel), each by a lane of its own, which also leaves the
-    // block's scales for the softmax -----------------------------------------------------------------------
-    Ring at;
-    int g = 0;
-    bool ok = true;
-    const int nb = kTile >> a.log_t;
-    while (ok && walk.next(a, before, words, sg)) {
-      const int* table = a.table + (int64_t)sg.r.req * a.table_blocks;
-      const int idx0 = (sg.r.s0 >> a.log_t) + lane;
-      auto entry_of = [&](int t) {                     // this lane's block of tile t (as it is), -1: none
-        const int idx = idx0 + t * nb;
-        return lane < nb && t >= sg.t0 && t < sg.t1 && ((long long)idx << a.log_t) < sg.r.len ? table[idx % a.table_blocks] : -1;
-      };
-      struct Block {
-        int e;
-        float ks, vs;
-      };
-      auto block_of = [&](int e) {                     // -1 if it is not there; its scales
-        Block b{-1, 0.f, 0.f};
-        if (e != -1 && in_bounds(e >= 0 && e < a.n_blocks, a.err)) {
-          b.e = e;
-          b.ks = a.k_scale[(int64_t)e * a.n_kv + sg.head];
-          b.vs = a.v_scale[(int64_t)e * a.n_kv + sg.head];
-        }
-        return b;
-      };
-      auto copy = [&](const CUtensorMap* map, const Block& b, bool key) {
-        const int slot = at.slot;
-        if (at.fill > 0) ok = wait_bar_warp(&empty[slot], at.fill + 1, a.err);
-        if (!ok) return;
-        const uint32_t bar = smem_u32(&full[slot]);
-        const int n = __popc(__ballot_sync(0xffffffffu, b.e >= 0));
-        if (b.e >= 0) {
-          const uint32_t dst = smem_u32(ring + (size_t)slot * STAGE) + ((uint32_t)(lane * ROWB) << a.log_t);
-#pragma unroll
-          for (int p = 0; p < PANELS; p++) tma_load_5d(dst + p * PANEL, map, p * 128, 0, sg.head, b.e, a.layer, bar);
-        }
-        // The constants, behind the copies: their loads may still be under way. The softmax has read those that they
-        // replace: the ring of tiles is deeper than the copies run ahead. This stage was free, so the scores of the
-        // tile S / 2 back were issued, and the two score buffers let that happen when those of two tiles before it
-        // had been read, its constants with them.
-        if (key && lane < nb) {
-          float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (b.e >= 0) {
-            scale_terms(fmaxf(b.vs, __int_as_float((kMinScaleExp + 127) << 23)), c.y, c.z);
-            c.x = b.ks * a.scale_log2;
-            c.w = 1.f;
+    if (kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 0) {
+      // ---- copies: one per block of the tile (and 128-byte panel), each by a lane of its own, which also leaves the
+      // block's scales for the softmax -----------------------------------------------------------------------
+      Ring at;
+      int g = 0;
+      bool ok = true;
+      const int nb = kTile >> a.log_t;
+      while (ok && walk.next(a, before, words, sg)) {
+        const int* table = a.table + (int64_t)sg.r.req * a.table_blocks;
+        const int idx0 = (sg.r.s0 >> a.log_t) + lane;
+        auto entry_of = [&](int t) {                     // this lane's block of tile t (as it is), -1: none
+          const int idx = idx0 + t * nb;
+          return lane < nb && t >= sg.t0 && t < sg.t1 && ((long long)idx << a.log_t) < sg.r.len ? table[idx % a.table_blocks] : -1;
+        };
+        struct Block {
+          int e;
+          float ks, vs;
+        };
+        auto block_of = [&](int e) {                     // -1 if it is not there; its scales
+          Block b{-1, 0.f, 0.f};
+          if (e != -1 && in_bounds(e >= 0 && e < a.n_blocks, a.err)) {
+            b.e = e;
+            b.ks = a.k_scale[(int64_t)e * a.n_kv + sg.head];
+            b.vs = a.v_scale[(int64_t)e * a.n_kv + sg.head];
           }
-          rs.key[g % kConstRing][lane] = c;
-        }
-        __syncwarp();
-        // the only arrival of the fill, so none of its bytes can end it before
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * ((uint32_t)HD << a.log_t));
-        __syncwarp();
-        at.next(S);
-        if (key) g++;
-      };
-      // entries three tiles ahead, scales two ahead of the values: K of tile t + 1, then V of tile t
-      Block cur{-1, 0.f, 0.f}, nxt = cur;
-      int far = -1;
+          return b;
+        };
+        auto copy = [&](const CUtensorMap* map, const Block& b, bool key) {
+          const int slot = at.slot;
+          if (at.fill > 0) ok = wait_bar_warp(&empty[slot], at.fill + 1, a.err);
+          if (!ok) return;
+          const uint32_t bar = smem_u32(&full[slot]);
+          const int n = __popc(__ballot_sync(0xffffffffu, b.e >= 0));
+          if (b.e >= 0) {
+            const uint32_t dst = smem_u32(ring + (size_t)slot * STAGE) + ((uint32_t)(lane * ROWB) << a.log_t);
+#pragma unroll
+            for (int p = 0; p < PANELS; p++) tma_load_5d(dst + p * PANEL, map, p * 128, 0, sg.head, b.e, a.layer, bar);
+          }
+          // The constants, behind the copies: their loads may still be under way. The softmax has read those that they
+          // replace: the ring of tiles is deeper than the copies run ahead. This stage was free, so the scores of the
+          // tile S / 2 back were issued, and the two score buffers let that happen when those of two tiles before it
+          // had been read, its constants with them.
+          if (key && lane < nb) {
+            float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (b.e >= 0) {
+              scale_terms(fmaxf(b.vs, __int_as_float((kMinScaleExp + 127) << 23)), c.y, c.z);
+              c.x = b.ks * a.scale_log2;
+              c.w = 1.f;
+            }
+            rs.key[g % kConstRing][lane] = c;
+          }
+          __syncwarp();
+          // the only arrival of the fill, so none of its bytes can end it before
+          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)n * ((uint32_t)HD << a.log_t));
+          __syncwarp();
+          at.next(S);
+          if (key) g++;
+        };
+        // entries three tiles ahead, scales two ahead of the values: K of tile t + 1, then V of tile t
+        Block cur{-1, 0.f, 0.f}, nxt = cur;
+        int far = -1;
 #pragma unroll 1
-      for (int t = sg.t0 - 3; ok && t < sg.t1; t++) {
-        const Block after = block_of(far);
-        far = entry_of(t + 3);
+        for (int t = sg.t0 - 3; ok && t < sg.t1; t++) {
+          const Block after = block_of(far);
+          far = entry_of(t + 3);
 #pragma unroll 1
-        for (int side = 0; ok && side < 2; side++) {
-          if (side == 0 ? t + 1 < sg.t0 || t + 1 >= sg.t1 : t < sg.t0) continue;
-          copy(side == 0 ? &kmap : &vmap, side == 0 ? nxt : cur, side == 0);
+          for (int side = 0; ok && side < 2; side++) {
+            if (side == 0 ? t + 1 < sg.t0 || t + 1 >= sg.t1 : t < sg.t0) continue;
+            copy(side == 0 ? &kmap : &vmap, side == 0 ? nxt : cur, side == 0);
+          }
+          cur = nxt;
+          nxt = after;
         }
-        cur = nxt;
-        nxt = after;
       }
-    }
-    // no copy may be in flight when the CTA leaves: the last fill of every stage has landed
-    for (int i = 0; i < S; i++) {
-      const int fills = at.fill + (i < at.slot);
-      if (fills > 0) wait_bar(&full[i], fills - 1, nullptr);
-    }
-  } else if (warp == 1) {
-    // ---- MMAs ---------------------------------------------------------------------------------------------
-    const uint32_t id_s = idesc_e4m3(NS, false), id_o = idesc_e4m3(N, true);
-    const uint32_t ring_a = smem_u32(ring);
-    const uint64_t qd0 = smem_desc(smem_u32(q_s), 16, 1024, 2), pd = smem_desc(smem_u32(p_s), 16, 1024, 2);
-    Ring at;                                           // consumed in the order of the copies
-    int g = 0, n_seg = 0, pv_done = 0;                 // g: tiles so far
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, int parity) { return wait_bar_warp(bar, parity, a.err); };
-    while (ok && walk.next(a, before, words, sg)) {
-      const int n = sg.t1 - sg.t0;
-      const uint64_t qd = qd0 + (uint64_t)((n_seg & 1) * (q_bytes >> 4));
-      ok = n_seg == 0 ? wait(q_first, 0) : wait(&q_full[n_seg & 1], (n_seg - 1) >> 1);
-      auto scores = [&](int t) {                       // tile t of the segment
-        const int slot = at.slot, gg = g + t;
-        ok = ok && wait(&full[slot], at.fill);
-        if (ok && gg >= 2) ok = wait(&s_free[gg & 1], (gg >> 1) + 1);
-        if (!ok) return;
-        tc05_fence_after();
-        const uint64_t kd = HD == 64 ? smem_desc(ring_a + slot * STAGE, 16, 512, 4) : smem_desc(ring_a + slot * STAGE, 16, 1024, 2);
-        const uint32_t d = tmem + (uint32_t)((gg & 1) * NS);
-#pragma unroll
-        for (int ks = 0; ks < HD / 32; ks++) {
-          const uint64_t ka = kd + (uint64_t)((ks / 4) * (PANEL >> 4) + (ks % 4) * 2);
-          const uint64_t qa = qd + (uint64_t)((ks / 4) * (N * 8) + (ks % 4) * 2);
-#pragma unroll
-          for (int i = 0; i < TERMS; i++) umma_e4m3_warp(d, ka, qa + (uint64_t)(i * RP * 8), id_s, ks > 0 || i > 0);
-        }
-        umma_commit_warp(smem_u32(&empty[slot]));
-        umma_commit_warp(smem_u32(&s_full[gg & 1]));
-        if (t + 1 == n) umma_commit_warp(smem_u32(&q_free[n_seg & 1]));
-        if (lane == 0) mbar_arrive(smem_u32(&s_full[gg & 1]));   // passes the copy warp's constants on
-        __syncwarp();
-        at.next(S);
-      };
-#pragma unroll 1
-      for (int t = -1; ok && t < n; t++) {
-        if (t + 1 < n) scores(t + 1);
-        if (t < 0) continue;
-        const int slot = at.slot, gg = g + t;
-        ok = ok && wait(&full[slot], at.fill) && wait(p_full, gg);
-        if (!ok) break;
-        tc05_fence_after();
-        const uint32_t va = ring_a + slot * STAGE;
-        const uint64_t vd = HD == 64 ? smem_desc(va, STAGE, 512, 4) : smem_desc(va, 16, 1024, 2);
-#pragma unroll
-        for (int p = 0; p < PANELS; p++)
-#pragma unroll
-          for (int ks = 0; ks < 4; ks++)
-            umma_e4m3_warp(tmem_o + p * N, vd + (uint64_t)((p * PANEL + ks * 32 * ROWB) >> 4), pd + (uint64_t)((ks * 32 * 128) >> 4),
-                           id_o, t > 0 || ks > 0);
-        umma_commit_warp(smem_u32(&empty[slot]));
-        umma_commit_warp(smem_u32(p_free));
-        pv_done = gg + 1;
-        at.next(S);
+      // no copy may be in flight when the CTA leaves: the last fill of every stage has landed
+      for (int i = 0; i < S; i++) {
+        const int fills = at.fill + (i < at.slot);
+        if (fills > 0) wait_bar(&full[i], fills - 1, nullptr);
       }
-      g += n;
-      n_seg++;
-    }
-    // nothing of this CTA may still run on the tensor core when its memory is freed. After a wait that gave up
-    // there may be scores without a probability product: their commits have a barrier of their own
-    if (pv_done > 0) wait_bar(p_free, pv_done - 1, a.err);
-    if (!ok) {
-      umma_commit_warp(smem_u32(drained));
-      wait_bar(drained, 0, nullptr);
-    }
+    } else if (warp == 1) {
+      // ---- MMAs ---------------------------------------------------------------------------------------------
+      const uint32_t id_s = idesc_e4m3(NS, false), id_o = idesc_e4m3(N, true);
+      const uint32_t ring_a = smem_u32(ring);
+      const uint64_t qd0 = smem_desc(smem_u32(q_s), 16, 1024, 2), pd = smem_desc(smem_u32(p_s), 16, 1024, 2);
+      Ring at;                                           // consumed in the order of the copies
+      int g = 0, n_seg = 0, pv_done = 0;                 // g: tiles so far
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int parity) { return wait_bar_warp(bar, parity, a.err); };
+      while (ok && walk.next(a, before, words, sg)) {
+        const int n = sg.t1 - sg.t0;
+        const uint64_t qd = qd0 + (uint64_t)((n_seg & 1) * (q_bytes >> 4));
+        ok = n_seg == 0 ? wait(q_first, 0) : wait(&q_full[n_seg & 1], (n_seg - 1) >> 1);
+        auto scores = [&](int t) {                       // tile t of the segment
+          const int slot = at.slot, gg = g + t;
+          ok = ok && wait(&full[slot], at.fill);
+          if (ok && gg >= 2) ok = wait(&s_free[gg & 1], (gg >> 1) + 1);
+          if (!ok) return;
+          tc05_fence_after();
+          const uint64_t kd = HD == 64 ? smem_desc(ring_a + slot * STAGE, 16, 512, 4) : smem_desc(ring_a + slot * STAGE, 16, 1024, 2);
+          const uint32_t d = tmem + (uint32_t)((gg & 1) * NS);
+#pragma unroll
+          for (int ks = 0; ks < HD / 32; ks++) {
+            const uint64_t ka = kd + (uint64_t)((ks / 4) * (PANEL >> 4) + (ks % 4) * 2);
+            const uint64_t qa = qd + (uint64_t)((ks / 4) * (N * 8) + (ks % 4) * 2);
+#pragma unroll
+            for (int i = 0; i < TERMS; i++) umma_e4m3_warp(d, ka, qa + (uint64_t)(i * RP * 8), id_s, ks > 0 || i > 0);
+          }
+          umma_commit_warp(smem_u32(&empty[slot]));
+          umma_commit_warp(smem_u32(&s_full[gg & 1]));
+          if (t + 1 == n) umma_commit_warp(smem_u32(&q_free[n_seg & 1]));
+          if (lane == 0) mbar_arrive(smem_u32(&s_full[gg & 1]));   // passes the copy warp's constants on
+          __syncwarp();
+          at.next(S);
+        };
+#pragma unroll 1
+        for (int t = -1; ok && t < n; t++) {
+          if (t + 1 < n) scores(t + 1);
+          if (t < 0) continue;
+          const int slot = at.slot, gg = g + t;
+          ok = ok && wait(&full[slot], at.fill) && wait(p_full, gg);
+          if (!ok) break;
+          tc05_fence_after();
+          const uint32_t va = ring_a + slot * STAGE;
+          const uint64_t vd = HD == 64 ? smem_desc(va, STAGE, 512, 4) : smem_desc(va, 16, 1024, 2);
+#pragma unroll
+          for (int p = 0; p < PANELS; p++)
+#pragma unroll
+            for (int ks = 0; ks < 4; ks++)
+              umma_e4m3_warp(tmem_o + p * N, vd + (uint64_t)((p * PANEL + ks * 32 * ROWB) >> 4), pd + (uint64_t)((ks * 32 * 128) >> 4),
+                             id_o, t > 0 || ks > 0);
+          umma_commit_warp(smem_u32(&empty[slot]));
+          umma_commit_warp(smem_u32(p_free));
+          pv_done = gg + 1;
+          at.next(S);
+        }
+        g += n;
+        n_seg++;
+      }
+      // nothing of this CTA may still run on the tensor core when its memory is freed. After a wait that gave up
+      // there may be scores without a probability product: their commits have a barrier of their own
+      if (pv_done > 0) wait_bar(p_free, pv_done - 1, a.err);
+      if (!ok) {
+        umma_commit_warp(smem_u32(drained));
+        wait_bar(drained, 0, nullptr);
+      }
   } else {
     // ---- queries of the later segments, while the one before is at work ---------------------------------------
     bool ok = true;
@@ -817,32 +836,30 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
         float2 x[CH * 4];
         uint32_t high = 0;                               // chunks of rows with an x above kMax
         const uint32_t ts = tmem + lanes + (uint32_t)((gg & 1) * NS);
-        {
-          uint32_t s8[CH][8];
+        uint32_t s8[CH][8];
 #pragma unroll
-          for (int ch = 0; ch < CH; ch++) tmem_start8(ts + ch * 8, s8[ch]);
+        for (int ch = 0; ch < CH; ch++) tmem_start8(ts + ch * 8, s8[ch]);
 #pragma unroll
-          for (int ch = 0; ch < CH; ch++) tmem_wait8(s8[ch]);
-          tc05_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&s_free[gg & 1]));
+        for (int ch = 0; ch < CH; ch++) tmem_wait8(s8[ch]);
+        tc05_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s_free[gg & 1]));
 #pragma unroll
-          for (int ch = 0; ch < CH; ch++) {
-            const float4* qp = reinterpret_cast<const float4*>(row_qs + ch * 8);
-            const float4* mp = reinterpret_cast<const float4*>(&rs.neg_m[ch * 8]);
-            const float4 q0 = qp[0], q1 = qp[1], m0 = mp[0], m1 = mp[1];
-            const float2 q2[4] = {{q0.x, q0.y}, {q0.z, q0.w}, {q1.x, q1.y}, {q1.z, q1.w}};
-            const float2 m2[4] = {{m0.x, m0.y}, {m0.z, m0.w}, {m1.x, m1.y}, {m1.z, m1.w}};
-            float top = -INFINITY;
+        for (int ch = 0; ch < CH; ch++) {
+          const float4* qp = reinterpret_cast<const float4*>(row_qs + ch * 8);
+          const float4* mp = reinterpret_cast<const float4*>(&rs.neg_m[ch * 8]);
+          const float4 q0 = qp[0], q1 = qp[1], m0 = mp[0], m1 = mp[1];
+          const float2 q2[4] = {{q0.x, q0.y}, {q0.z, q0.w}, {q1.x, q1.y}, {q1.z, q1.w}};
+          const float2 m2[4] = {{m0.x, m0.y}, {m0.z, m0.w}, {m1.x, m1.y}, {m1.z, m1.w}};
+          float top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-              const float2 sc = make_float2(__uint_as_float(s8[ch][2 * j]), __uint_as_float(s8[ch][2 * j + 1]));
-              const float2 v = fma2(mul2(sc, q2[j]), ka, add2(vb2, m2[j]));
-              x[ch * 4 + j] = v;
-              top = fmaxf(top, fmaxf(v.x, v.y));
-            }
-            if (top > kMax) high |= 1u << ch;
+          for (int j = 0; j < 4; j++) {
+            const float2 sc = make_float2(__uint_as_float(s8[ch][2 * j]), __uint_as_float(s8[ch][2 * j + 1]));
+            const float2 v = fma2(mul2(sc, q2[j]), ka, add2(vb2, m2[j]));
+            x[ch * 4 + j] = v;
+            top = fmaxf(top, fmaxf(v.x, v.y));
           }
+          if (top > kMax) high |= 1u << ch;
         }
         if (edge) {
           high = 0;
@@ -926,28 +943,26 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
         __syncwarp();
 #pragma unroll
         for (int ch = 0; ch < CH; ch++) {
-          {
-            float2 w[4];
+          float2 w[4];
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-              w[j] = make_float2(ex2(x[ch * 4 + j].x), ex2(x[ch * 4 + j].y));
-              l[ch * 4 + j] = fma2(w[j], inv2, l[ch * 4 + j]);
-            }
-            // columns of the product: per chunk of rows, its terms side by side (with two terms one 16-byte piece)
-            uint2 c[TERMS];
-            split8<TERMS>(w, c);
-            if constexpr (TERMS == 2) {
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + (uint32_t)((ch ^ (key & 7)) << 4)), "r"(c[0].x),
-                           "r"(c[0].y), "r"(c[1].x), "r"(c[1].y)
+          for (int j = 0; j < 4; j++) {
+            w[j] = make_float2(ex2(x[ch * 4 + j].x), ex2(x[ch * 4 + j].y));
+            l[ch * 4 + j] = fma2(w[j], inv2, l[ch * 4 + j]);
+          }
+          // columns of the product: per chunk of rows, its terms side by side (with two terms one 16-byte piece)
+          uint2 c[TERMS];
+          split8<TERMS>(w, c);
+          if constexpr (TERMS == 2) {
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + (uint32_t)((ch ^ (key & 7)) << 4)), "r"(c[0].x),
+                         "r"(c[0].y), "r"(c[1].x), "r"(c[1].y)
+                         : "memory");
+          } else {
+#pragma unroll
+            for (int i = 0; i < TERMS; i++) {
+              const int o = (ch * TERMS + i) * 8;
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(p_row + (uint32_t)((((o >> 4) ^ (key & 7)) << 4) + (o & 8))),
+                           "r"(c[i].x), "r"(c[i].y)
                            : "memory");
-            } else {
-#pragma unroll
-              for (int i = 0; i < TERMS; i++) {
-                const int o = (ch * TERMS + i) * 8;
-                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(p_row + (uint32_t)((((o >> 4) ^ (key & 7)) << 4) + (o & 8))),
-                             "r"(c[i].x), "r"(c[i].y)
-                             : "memory");
-              }
             }
           }
         }
@@ -962,12 +977,11 @@ __global__ void __launch_bounds__(kThreads, RP <= kRowsOfTwo ? 2 : 1)
 
       // ---- end of the segment: L over the keys, then O -------------------------------------------------------
 #pragma unroll
-      for (int ch = 0; ch < CH; ch++)
-        {
-          const float v8[8] = {l[4 * ch].x, l[4 * ch].y, l[4 * ch + 1].x, l[4 * ch + 1].y, l[4 * ch + 2].x, l[4 * ch + 2].y, l[4 * ch + 3].x, l[4 * ch + 3].y};
-          const float sum = reduce8(v8, [](float p, float q) { return p + q; });
-          if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = sum;
-        }
+      for (int ch = 0; ch < CH; ch++) {
+        const float v8[8] = {l[4 * ch].x, l[4 * ch].y, l[4 * ch + 1].x, l[4 * ch + 1].y, l[4 * ch + 2].x, l[4 * ch + 2].y, l[4 * ch + 3].x, l[4 * ch + 3].y};
+        const float sum = reduce8(v8, [](float p, float q) { return p + q; });
+        if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = sum;
+      }
       wait(p_free, g - 1);
       softmax_sync();
       gone = dead[look++ & 1];
@@ -1047,14 +1061,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR;
   const int pair = blockIdx.x, per_req = a.n_kv * a.p.chunks, b = pair / per_req, in_req = pair - b * per_req;
   const int head = in_req / a.p.chunks, chunk = in_req - head * a.p.chunks;
-  const int total = a.units[a.n_req], first = a.units[b];
-  const Request rq = request_of(a, read_request(a, b));
+  const int total = a.units[a.n_req], first = a.units[b], setup = a.units[a.n_req + 1];
+  const Request rq = request_of(a, a.words[b]);
   const int rows = min(a.p.rc, rq.n * a.grp - chunk * a.p.rc), r_cta = blockIdx.y * join_rows(HD);
   if (r_cta >= rows) return;
   const int ctas = min(a.grid, total);
   int c0 = 0, c1 = -1;                                 // CTAs that hold tiles of these rows
   if (rq.tiles > 0) {
-    const long long s = first + (long long)(head * rq.chunks + chunk) * rq.tiles, e = s + rq.tiles;
+    const long long s = first + (long long)(head * rq.chunks + chunk) * (rq.tiles + setup) + setup, e = s + rq.tiles;
     c0 = (int)(((s + 1) * ctas - 1) / total);
     c1 = (int)((e * ctas - 1) / total);
     if (c0 == c1 && !a.k_own) return;                  // written by the first kernel
@@ -1198,7 +1212,7 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtens
   static std::atomic<int> smem_set[kMaxDevices];
   cudaError_t e = ensure_smem_limit(cache_attn_kernel<T, HD, RP>, a.p.smem, smem_set);
   if (e != cudaSuccess) return e;
-  if (RP > 8 && RP <= kRowsOfTwo) {   // the softmax warps would wait for registers that the CTA does not have
+  if (RP > 8 && two_per_sm(HD, RP)) {   // the softmax warps would wait for registers that the CTA does not have
     static const int regs = [] {
       cudaFuncAttributes at{};
       return cudaFuncGetAttributes(&at, cache_attn_kernel<T, HD, RP>) == cudaSuccess ? at.numRegs : 0;
@@ -1218,7 +1232,11 @@ cudaError_t launch_rows(const CacheAttnArgs& a, const CUtensorMap& kmap, const C
     case 8: return launch<T, HD, 8>(a, kmap, vmap, s);
     case 16: return launch<T, HD, 16>(a, kmap, vmap, s);
     case 24: return launch<T, HD, 24>(a, kmap, vmap, s);
+    case 32: return launch<T, HD, 32>(a, kmap, vmap, s);
     case 40: return launch<T, HD, 40>(a, kmap, vmap, s);
+    case 48:
+      if constexpr (__is_same(T, __nv_bfloat16)) return launch<T, HD, 48>(a, kmap, vmap, s);
+      break;
     case 64:
       if constexpr (__is_same(T, __nv_bfloat16)) return launch<T, HD, 64>(a, kmap, vmap, s);
   }
@@ -1244,7 +1262,7 @@ CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req) 
   const int limit = dtype == DFLASH_BF16 ? 64 : 40, rows = grp * max_q;
   p.chunks = (rows + limit - 1) / limit;
   p.rc = (rows + p.chunks - 1) / p.chunks;
-  p.rp = p.rc <= 8 ? 8 : p.rc <= 16 ? 16 : p.rc <= 24 ? 24 : p.rc <= 40 ? 40 : 64;   // the kernels there are
+  p.rp = p.rc <= 8 ? 8 : p.rc <= 16 ? 16 : p.rc <= 24 ? 24 : p.rc <= 32 ? 32 : p.rc <= 40 ? 40 : p.rc <= 48 ? 48 : 64;   // the kernels there are
   p.n = weight_columns(p.terms, p.rp);
   p.ns = score_columns(p.rp);
   const int cols = 2 * p.ns + panels_of(hd) * p.n;
@@ -1254,7 +1272,11 @@ CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req) 
   constexpr size_t kPerSm = 227 * 1024;
   // two CTAs per SM where registers and tensor memory allow it and each still holds four key or value tiles
   const size_t half = kPerSm / 2 - 1024;
-  p.ctas_per_sm = p.rp <= kRowsOfTwo && p.tmem_cols <= 256 && fixed + 4 * (size_t)stage_bytes(hd) <= half ? 2 : 1;
+  // 32 requests x 5 rows over 512 to 2048 keys: 50.0 us if it counts nothing, 47.1 as 2 tiles, 46.5 as 3, 46.2 as 4; 16 x 9
+  // causal rows over 500 to 8192: 70.9, 57.5, 55.7, 55.6, with 256 columns 66.4, 54.9, 53.4, 47.7; one request's 264
+  // tiles: 15.5 us up to 3, 17.7 as 4.
+  p.setup = hd == 256 ? 4 : 3;
+  p.ctas_per_sm = two_per_sm(hd, p.rp) && p.tmem_cols <= 256 && fixed + 4 * (size_t)stage_bytes(hd) <= half ? 2 : 1;
   const size_t room = (p.ctas_per_sm == 2 ? half : kPerSm) - fixed;
   p.stages = (int)std::min<size_t>(kMaxStages, room / stage_bytes(hd));
   p.smem = fixed + (size_t)p.stages * stage_bytes(hd);
