@@ -48,7 +48,10 @@ constexpr int kSoftmax0 = 128;           // first softmax thread
 constexpr int kStartRegs = 128, kOtherRegs = 96, kSoftmaxRegs = 160;
 static_assert(kOtherRegs + kSoftmaxRegs <= 2 * kStartRegs, "the shares come out of what the CTA was launched with");
 constexpr int kConstRing = 16;           // tiles whose key constants are kept
-constexpr int kMaxStages = 12;
+// Key and value tiles in flight. Four for few rows, bound by the bytes: 32 single tokens over 512 to 16384 keys take
+// 89.7 us, 91.4 with six, 91.9 with three. Three for more rows, whose first tiles then come sooner: 4 requests x 8 rows
+// over 2000 to 9000 keys 26.5 us, 28.0 with four; with 256 columns (16 x 9 rows) 47.5 us, 47.0 with four.
+constexpr int kMaxStages = 4;
 constexpr int kPBytes = kTile * 128;     // probabilities: 128 keys x up to 128 columns
 constexpr float kTop = 5.f, kMax = 8.75f;
 constexpr float kUnset = -1e30f;         // reference of a piece whose row has seen no key
@@ -517,9 +520,6 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
   __syncthreads();
   tc05_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // Later kernels may start only now that this CTA holds its tensor memory: one that took it first would wait for
-  // this kernel, which would wait for it.
-  pdl_launch_dependents();
   pdl_wait();
   // units before each request: one prefix sum over the requests, a few of them per thread, of the key tiles (low half)
   // and the setups (high half)
@@ -1033,6 +1033,9 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
     }
   }
 
+  // Only now: CTAs that wait beside this one slow its end (one request, 8 rows: 15.5 us against 14.8), and one that took
+  // the tensor memory before a CTA of this kernel would wait for it, and it for this one.
+  pdl_launch_dependents();
   tc05_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -1270,7 +1273,7 @@ CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req) 
   while (p.tmem_cols < cols) p.tmem_cols *= 2;
   const size_t fixed = attn_fixed_smem(hd, p.n, n_req) + 1024;
   constexpr size_t kPerSm = 227 * 1024;
-  // two CTAs per SM where registers and tensor memory allow it and each still holds four key or value tiles
+  // two CTAs per SM where registers and tensor memory allow it and each holds four key or value tiles
   const size_t half = kPerSm / 2 - 1024;
   // 32 requests x 5 rows over 512 to 2048 keys: 50.0 us if it counts nothing, 47.1 as 2 tiles, 46.5 as 3, 46.2 as 4; 16 x 9
   // causal rows over 500 to 8192: 70.9, 57.5, 55.7, 55.6, with 256 columns 66.4, 54.9, 53.4, 47.7; one request's 264
@@ -1278,7 +1281,7 @@ CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req) 
   p.setup = hd == 256 ? 4 : 3;
   p.ctas_per_sm = two_per_sm(hd, p.rp) && p.tmem_cols <= 256 && fixed + 4 * (size_t)stage_bytes(hd) <= half ? 2 : 1;
   const size_t room = (p.ctas_per_sm == 2 ? half : kPerSm) - fixed;
-  p.stages = (int)std::min<size_t>(kMaxStages, room / stage_bytes(hd));
+  p.stages = (int)std::min<size_t>(hd == 256 || p.rp == 8 ? kMaxStages : 3, room / stage_bytes(hd));
   p.smem = fixed + (size_t)p.stages * stage_bytes(hd);
   return p;
 }
