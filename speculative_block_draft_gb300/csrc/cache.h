@@ -54,7 +54,7 @@ struct CacheAttnArgs {
   CacheAttnPlan p;
   int grid;                                        // CTAs of the first kernel
   int4* words;                                     // [n_req] what the call says about each request (read_request)
-  int* units;                                      // [n_req + 1] units before each request, and those of a setup
+  int2* held_by;                                   // [n_req * n_kv * chunks] first and last CTA with tiles
   float* part_o;                                   // [grid + n_req * n_kv * chunks][rp][hd]
   float2* part_ml;                                 // [..][rp] (reference, sum)
 };

@@ -15,7 +15,8 @@ struct dflash_cache {
   int device = 0, log_t = 0;
   unsigned* err = nullptr;      // [0] error bits, [1] wait limit in us (0: 1 s)
   int n_sm = 148;
-  int4* requests = nullptr;     // [max_requests], then units: [max_requests + 2] ints
+  int4* requests = nullptr;     // [max_requests]
+  int2* held_by = nullptr;      // [requests x KV heads x row chunks]
   float2* part_ml = nullptr;    // attention pieces: rows of (reference, sum), then of head_dim floats
   float* part_o = nullptr;
   int64_t part_rows = 0;
@@ -59,7 +60,7 @@ int64_t piece_rows(const dflash_cache_config& f, int n_sm) {
 
 size_t round_256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// Workspace: error word | requests and units | (m, L) of the pieces | O of the pieces.
+// Workspace: error word | requests | their pieces' CTAs | (m, L) of the pieces | O of the pieces.
 size_t carve(dflash_cache* c, uint8_t* base) {
   const dflash_cache_config& f = c->cfg;
   size_t at = 256;
@@ -67,7 +68,9 @@ size_t carve(dflash_cache* c, uint8_t* base) {
   if (f.max_requests) {
     c->part_rows = piece_rows(f, c->n_sm);
     c->requests = reinterpret_cast<int4*>(base + at);
-    at += round_256(16 * (size_t)f.max_requests + 4 * (size_t)(f.max_requests + 2));
+    at += round_256(16 * (size_t)f.max_requests);
+    c->held_by = reinterpret_cast<int2*>(base + at);
+    at += round_256(8 * (size_t)f.max_requests * f.n_kv_heads * (((size_t)(f.n_q_heads / f.n_kv_heads) * f.max_q + 39) / 40));
     c->part_ml = reinterpret_cast<float2*>(base + at);
     at += round_256(8 * (size_t)c->part_rows);
     c->part_o = reinterpret_cast<float*>(base + at);
@@ -261,7 +264,7 @@ int dflash_cache_attention(dflash_cache* c, const dflash_attention* p, void* str
   a.grid = (int)std::min<int64_t>((int64_t)a.p.ctas_per_sm * c->n_sm, tiles);
   if ((a.grid + pairs) * a.p.rp > c->part_rows) return DFLASH_ECAPACITY;
   a.words = c->requests;
-  a.units = reinterpret_cast<int*>(c->requests + f.max_requests);
+  a.held_by = c->held_by;
   a.part_o = c->part_o;
   a.part_ml = c->part_ml;
   return status_of(launch_cache_attn(p->dtype, a, c->kmap, c->vmap, static_cast<cudaStream_t>(stream)));

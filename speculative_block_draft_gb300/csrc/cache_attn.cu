@@ -129,7 +129,10 @@ __device__ __forceinline__ Request request_of(const CacheAttnArgs& a, int4 w) {
 // A CTA's run is units [first, last) of all; CTA c of g gets an equal share. A (request, KV head, row chunk) is
 // `setup` units, which stand for its queries, its first references and its output, then its key tiles. They count
 // nothing where there is a CTA for every tile.
-__device__ __forceinline__ long long unit_begin(int c, int total, int g) { return (long long)c * total / g; }
+__device__ __forceinline__ int unit_begin(int c, int total, int g) {
+  const int each = total / g;
+  return c * each + min(c, total - each * g);
+}
 
 // The tiles of one (request, KV head, row chunk) that a CTA's run holds.
 struct Segment {
@@ -566,14 +569,11 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
   __syncthreads();
   const int total = before[a.n_req], ctas = min(a.grid, total);
   if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b <= a.n_req + 1; b += kThreads) {   // for the second kernel
-      if (b < a.n_req) a.words[b] = words[b];
-      a.units[b] = before[b];
-    }
+    for (int b = threadIdx.x; b < a.n_req; b += kThreads) a.words[b] = words[b];   // for the second kernel
   Walk walk{0, 0, 0};
   if ((int)blockIdx.x < ctas) {
-    walk.u = (int)unit_begin(blockIdx.x, total, ctas);
-    walk.u_end = (int)unit_begin(blockIdx.x + 1, total, ctas);
+    walk.u = unit_begin(blockIdx.x, total, ctas);
+    walk.u_end = unit_begin(blockIdx.x + 1, total, ctas);
     int lo = 0, hi = a.n_req;                          // the request that holds the first unit
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -989,6 +989,10 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
       if (threadIdx.x == kSoftmax0) mbar_arrive(smem_u32(&q_free[n_seg & 1]));
       const bool direct = sg.t0 == 0 && sg.t1 == sg.r.tiles && !a.k_own;
       const size_t slot = (size_t)blockIdx.x + sg.pair;
+      if (threadIdx.x == kSoftmax0) {                  // which CTAs hold the pair's tiles
+        if (sg.t0 == 0) a.held_by[sg.pair].x = blockIdx.x;
+        if (sg.t1 == sg.r.tiles) a.held_by[sg.pair].y = blockIdx.x;
+      }
       if (key < RP) {
         const float L = (rs.red[0][key] + rs.red[1][key]) + (rs.red[2][key] + rs.red[3][key]);
         rs.f[key] = L == 0.f ? 0.f : 1.f / L;
@@ -1064,18 +1068,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR;
   const int pair = blockIdx.x, per_req = a.n_kv * a.p.chunks, b = pair / per_req, in_req = pair - b * per_req;
   const int head = in_req / a.p.chunks, chunk = in_req - head * a.p.chunks;
-  const int total = a.units[a.n_req], first = a.units[b], setup = a.units[a.n_req + 1];
+  const int2 by = a.held_by[pair];
   const Request rq = request_of(a, a.words[b]);
   const int rows = min(a.p.rc, rq.n * a.grp - chunk * a.p.rc), r_cta = blockIdx.y * join_rows(HD);
   if (r_cta >= rows) return;
-  const int ctas = min(a.grid, total);
-  int c0 = 0, c1 = -1;                                 // CTAs that hold tiles of these rows
-  if (rq.tiles > 0) {
-    const long long s = first + (long long)(head * rq.chunks + chunk) * (rq.tiles + setup) + setup, e = s + rq.tiles;
-    c0 = (int)(((s + 1) * ctas - 1) / total);
-    c1 = (int)((e * ctas - 1) / total);
-    if (c0 == c1 && !a.k_own) return;                  // written by the first kernel
-  }
+  const int c0 = rq.tiles > 0 ? by.x : 0, c1 = rq.tiles > 0 ? by.y : -1;   // CTAs that hold tiles of these rows
+  if (c0 == c1 && !a.k_own) return;                    // written by the first kernel
   const int r = min(r_cta + warp * (32 / LPR) + lane / LPR, rows - 1);    // spare lanes repeat the last row
   const bool live = r == r_cta + warp * (32 / LPR) + lane / LPR;
   const int rr = chunk * a.p.rc + r, i = by_group(a, rr), qh = head * a.grp + rr - i * a.grp, row = rq.row0 + i;
