@@ -472,7 +472,7 @@ typedef struct {
   float scale;
 } dflash_attention;
 
-/* Rows that see no key get zeros. Keys whose table entry is out of range are not seen, nor are those that
+/* Rows that see no key get zeros. out may be q. Keys whose table entry is out of range are not seen, nor are those that
  * a ring no longer holds (before len - table_blocks * T). What masked keys' blocks hold does not matter; a
  * NaN in a value that some rows of a request see and others do not makes the whole output row of those
  * that see it NaN. Rounding: queries and probabilities enter the tensor

@@ -63,6 +63,8 @@ class BlockPool:
     def __init__(self, block_tokens: int, max_requests: int | None = None, ring: bool = False, device="cuda"):
         if block_tokens not in (16, 32, 64, 128) or (max_requests is not None and not 0 < max_requests <= DFLASH_POOL_MAX_REQUESTS):
             raise DFlashError(DFLASH_EINVAL, "BlockPool")
+        if torch.device(device).type != "cuda":
+            raise ValueError(f"BlockPool: its tensors are on a CUDA device, not on {device}")
         self.block_tokens, self.ring, self.max_requests = block_tokens, int(ring), max_requests
         self.scratch = torch.zeros(DFLASH_POOL_SCRATCH, dtype=torch.uint8, device=device)
         self.device = self.scratch.get_device()
@@ -119,6 +121,8 @@ class Cache:
         nbytes = lib().dflash_cache_workspace_bytes(ctypes.byref(cfg))
         if nbytes == 0:
             raise DFlashError(DFLASH_EINVAL, "dflash_cache_workspace_bytes")
+        if not k.is_cuda or self.device != torch.cuda.current_device():
+            raise ValueError(f"the codes are on {k.device}, not on the current CUDA device")
         self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=k.device)
         base = (self.workspace.data_ptr() + 255) // 256 * 256
         h = ctypes.c_void_p()

@@ -19,13 +19,19 @@
 //   w_ij = 2^(t_ij - m_i)                       = p_ij * v_scale / 2^m_i
 //   O_i = sum_j w_ij * vcode_j,  L_i = sum_j w_ij / v_scale,  out_i = O_i / L_i
 // The reference m_i of a row is set so that its largest weight so far is 2^kTop, and moves only when a
-// weight would pass 2^kMax (kept below 448, the largest code): then L and O are rescaled. Weights of
-// 2^-4 and more keep all their bits; below, the subnormal codes' step of 2^-9 is the floor.
+// weight would pass 2^kMax (kept below 448, the largest code): then L and O are rescaled. Two terms hold 8 bits of a
+// weight of 2^-2 and more; below, the subnormal codes' step of 2^-9 leaves at most 2 * 2^-10, which is 2^-14 of the
+// row's largest weight. (kTop = 3 moves less often, 42 us against 42.5 for 32 requests x 5 rows, and leaves 2^-12.)
+//
+// What bounds it: the cache's bytes, in the steady state (32 requests, 8 KV heads of 128 columns: 6.8 TB/s with 25
+// rows per KV head, 6.5 with 40, 6.0 with 45, from the difference of 16384 and 8192 keys each), and before it some
+// 12 us (one row) to 20 us (five) of start, first references, output and second kernel, which short contexts feel.
 //
 // Work is split by key tiles, not by requests: all tiles of all (request, KV head, row chunk) in one
 // line, an equal run of them for each CTA. A run may begin or end inside a (request, head, chunk); those
 // pieces are left as (O, m, L) for the second kernel, which joins them and attends over the own rows
-// in fp32.
+// in fp32. (Joined instead by the CTA whose piece comes last: 54.8 us against 42.7 for 32 requests x 5 rows over 512 to
+// 2048 keys, 47.6 against 27.9 for 4 x 8 rows over 2000 to 9000. Its four warps have the rows' latency to themselves.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -465,8 +471,10 @@ __device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Se
   }
 }
 
-// RP: query rows of a chunk, padded. It is known here so that the loops over the rows have no branches: with one, every
-// eight rows would wait for their own loads.
+// RP: query rows of a chunk, padded to the next of 8, 16, 24, 32, 40, 48 (bf16) and 64 (bf16). It is known here so that
+// the loops over the rows have no branches: with one, every eight rows would wait for their own loads (32 requests x 25
+// rows 81 us; 64 without, and with weights split in fp32). 25 rows padded to 40 instead of 32 take 53.1 us against 49.5, 45 rows to 64 instead of 48 100
+// against 90.
 template <typename T, int HD, int RP>
 __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
     cache_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ CUtensorMap kmap,
@@ -1056,7 +1064,8 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
 constexpr int kJoinWarps = 8, kOwnTile = 16;           // own rows in shared memory at a time
 __host__ __device__ constexpr int join_rows(int hd) { return kJoinWarps * 256 / hd; }
 
-// kAtOnce: pieces in flight, eight where a row has many (a long context of few requests), else four for the occupancy.
+// kAtOnce: pieces in flight, eight where a row has many (one request x 8 rows over 2048 keys: 15.5 us, 16.3 with four),
+// else four for the occupancy (32 requests x 5 rows: 53.1 us, 57.3 with eight).
 template <typename T, int HD, int kAtOnce>
 __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
   constexpr int LPR = HD / 8;                          // lanes of a row
@@ -1072,7 +1081,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
   const Request rq = request_of(a, a.words[b]);
   const int rows = min(a.p.rc, rq.n * a.grp - chunk * a.p.rc), r_cta = blockIdx.y * join_rows(HD);
   if (r_cta >= rows) return;
-  const int c0 = rq.tiles > 0 ? by.x : 0, c1 = rq.tiles > 0 ? by.y : -1;   // CTAs that hold tiles of these rows
+  // CTAs that hold tiles of these rows (within the grid even if one gave up before it left its number)
+  const int c0 = rq.tiles > 0 ? max(by.x, 0) : 0, c1 = rq.tiles > 0 ? min(by.y, a.grid - 1) : -1;
   if (c0 == c1 && !a.k_own) return;                    // written by the first kernel
   const int r = min(r_cta + warp * (32 / LPR) + lane / LPR, rows - 1);    // spare lanes repeat the last row
   const bool live = r == r_cta + warp * (32 / LPR) + lane / LPR;
@@ -1259,7 +1269,7 @@ cudaError_t launch_hd(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUt
 CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req) {
   CacheAttnPlan p{};
   p.terms = dtype == DFLASH_BF16 ? 2 : 3;
-  // at most 128 MMA columns: then two score buffers and the output fit tensor memory for every head_dim
+  // at most 128 MMA columns of weights, a swizzled row: then two score buffers and the output fit tensor memory as well
   const int limit = dtype == DFLASH_BF16 ? 64 : 40, rows = grp * max_q;
   p.chunks = (rows + limit - 1) / limit;
   p.rc = (rows + p.chunks - 1) / p.chunks;
@@ -1271,7 +1281,8 @@ CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req) 
   while (p.tmem_cols < cols) p.tmem_cols *= 2;
   const size_t fixed = attn_fixed_smem(hd, p.n, n_req) + 1024;
   constexpr size_t kPerSm = 227 * 1024;
-  // two CTAs per SM where registers and tensor memory allow it and each holds four key or value tiles
+  // two CTAs per SM where registers and tensor memory allow it and each can hold four key or value tiles (one: 72 us
+  // against 53 for 32 requests x 5 rows, 36.5 against 30 for 4 x 8)
   const size_t half = kPerSm / 2 - 1024;
   // 32 requests x 5 rows over 512 to 2048 keys: 50.0 us if it counts nothing, 47.1 as 2 tiles, 46.5 as 3, 46.2 as 4; 16 x 9
   // causal rows over 500 to 8192: 70.9, 57.5, 55.7, 55.6, with 256 columns 66.4, 54.9, 53.4, 47.7; one request's 264

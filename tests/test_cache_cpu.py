@@ -119,6 +119,14 @@ def test_binding_refuses(lib):
         pkg.Cache(k, k, s, s, max_requests=4, max_q=2, n_q_heads=3)
 
 
+def test_binding_refuses_host_memory(lib):
+    k, s = torch.zeros((1, 4, 2, 16, 64), dtype=torch.uint8), torch.zeros((1, 4, 2))
+    with pytest.raises(ValueError):
+        pkg.Cache(k, k, s, s)
+    with pytest.raises(ValueError):
+        pkg.BlockPool(64, device="cpu")
+
+
 def test_reference_scale_and_codes():
     """The restatement's scale keeps every finite value in range and no smaller power of two does; a
     code is off by at most 2^-4 relative, or half the smallest code."""

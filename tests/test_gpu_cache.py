@@ -96,6 +96,17 @@ def test_reserve_many_rows():
     p.reserve([rng.randint(0, 30) for _ in range(1000)], requests=rng.sample(range(1024), 1000))
 
 
+def test_most_requests():
+    """As many requests as a call may have; released blocks of all of them by several CTAs."""
+    rng = random.Random(5)
+    p = Pool(16, 1024, 40, 30000, seed=6)
+    p.reserve([rng.choice((0, 1, 16, 17, 300, 640)) for _ in range(1024)])
+    p.truncate([rng.randint(0, 640) for _ in range(1024)])
+    p.reserve([rng.randint(0, 30) for _ in range(1024)])
+    p.truncate([0] * 1024)
+    assert p.count == 30000
+
+
 def test_ring_reuses_blocks():
     p, rng = Pool(16, 4, 5, 17, ring=True), random.Random(3)
     for n in (1, 70, 15, 64, 33, 300, 16):
@@ -182,6 +193,16 @@ def test_append_many_rows():
     check_append((k, v), (ks, vs), rows, slots, T)
 
 
+def test_append_skips_every_row():
+    T, N, H, D = 32, 5, 2, 128
+    dev = [x.cuda() for x in ref.random_cache(1, N, H, T, D, 1)]
+    before = [x.clone() for x in dev]
+    rows = torch.randn((700, H, D), device="cuda")
+    pkg.Cache(*dev).append(ints([-1] * 700), rows, rows)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, dev))
+
+
 def test_append_refuses():
     T, N, H, D = 16, 4, 2, 64
     k, v, ks, vs = (x.cuda() for x in ref.random_cache(1, N, H, T, D, 1))
@@ -262,6 +283,40 @@ def test_attention_many_rows(rows, Hq, H):
     """More query rows per KV head than one CTA holds."""
     run_attention([300, 140], [rows] * 2, Hq, H, 128, 64, "bf16", causal=True, seed=rows)
     run_attention([300, 140], [rows] * 2, Hq, H, 64, 32, "f16", own=True, seed=rows)
+
+
+@pytest.mark.parametrize("rows,Hq,H", [(5, 5, 1), (8, 8, 2), (11, 6, 2), (9, 5, 1), (12, 8, 2), (10, 10, 2)])
+@pytest.mark.parametrize("D,T,dtype", [(64, 16, "f16"), (64, 32, "bf16"), (128, 64, "f16"), (128, 128, "bf16"), (256, 32, "f16"), (256, 64, "bf16")])
+def test_attention_row_counts(rows, Hq, H, D, T, dtype):
+    """Every padding of the rows of a KV head: 25, 32, 33, 45, 48 and 50 of them."""
+    run_attention([390, 64, 1], [rows] * 3, Hq, H, D, T, dtype, causal=True, seed=rows)
+    run_attention([140, 0, 259], [rows] * 3, Hq, H, D, T, dtype, own=True, window=100, seed=rows)
+
+
+def test_attention_most_requests():
+    """As many requests as a call may have, more pieces of work than CTAs; some without rows, some without keys."""
+    rng = random.Random(3)
+    lens = [rng.choice((0, 1, 15, 16, 40, 130, 260)) for _ in range(1024)]
+    run_attention(lens, [rng.randint(0, 2) for _ in lens], 2, 1, 64, 16, "bf16", causal=True, seed=11)
+    run_attention(lens, [1] * 1024, 2, 2, 64, 16, "f16", own=True, window=20, seed=12)
+    run_attention([0] * 1024, [1] * 1024, 1, 1, 64, 16, "bf16", seed=13)
+
+
+def test_attention_names_a_request_twice():
+    run_attention([300, 20, 77], [3, 1, 4, 3], 6, 2, 128, 32, "bf16", own=True, requests=[2, 0, 2, 0], seed=14)
+
+
+def test_attention_writes_over_its_queries():
+    """out may be q: a row is written when nobody reads it any more."""
+    T, H, Hq, D, lens = 64, 2, 10, 128, [3000, 70, 900]
+    k, v, ks, vs = ref.random_cache(1, 66, H, T, D, 1)
+    table = ref.random_table(lens, T, 66, 47, 2)
+    q = torch.randn((12, Hq, D), generator=torch.Generator().manual_seed(3)).bfloat16()
+    cache = pkg.Cache(k.cuda(), v.cuda(), ks.cuda(), vs.cuda(), max_requests=3, max_q=4, n_q_heads=Hq)
+    out, apart = q.cuda(), torch.zeros_like(q, device="cuda")
+    cache.attention(q.cuda(), ints(lens), ints(table), apart, causal=True)
+    cache.attention(out, ints(lens), ints(table), out, causal=True)
+    assert torch.equal(out, apart)
 
 
 def test_attention_long_contexts():
