@@ -1061,16 +1061,17 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
 // takes some rows of one (request, KV head, chunk), a row in HD / 8 lanes of eight columns each, so that the own
 // rows' K/V are read once for all of them (a warp per row, each reading them all, took 18 us instead of 6 for 32
 // requests x 5 rows of 5 query heads).
-constexpr int kJoinWarps = 8, kOwnTile = 16;           // own rows in shared memory at a time
-__host__ __device__ constexpr int join_rows(int hd) { return kJoinWarps * 256 / hd; }
+constexpr int kOwnTile = 16;                           // own rows in shared memory at a time
+__host__ __device__ constexpr int join_rows(int hd, int warps) { return warps * 256 / hd; }
 
-// kAtOnce: pieces in flight, eight where a row has many (one request x 8 rows over 2048 keys: 15.5 us, 16.3 with four),
-// else four for the occupancy (32 requests x 5 rows: 53.1 us, 57.3 with eight).
-template <typename T, int HD, int kAtOnce>
-__global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
+// kAtOnce: pieces in flight, eight where a row has many (one request x 8 rows over 2048 keys: 14.4 us, 15.1 with four),
+// else four for the occupancy (32 requests x 5 rows: 41.0 us, 45.7 with eight). WARPS: four where they hold a chunk's
+// rows (one token over 1024 keys: 8.1 us, 8.5 with eight), else eight (4 requests x 8 rows: 25.7 us, 27.5 with four).
+template <typename T, int HD, int WARPS, int kAtOnce>
+__global__ void __launch_bounds__(WARPS * 32) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
   constexpr int LPR = HD / 8;                          // lanes of a row
   constexpr int kStep = LPR / 8;                       // lanes between the scores of neighbouring own rows
-  constexpr int kLoads = kOwnTile * LPR / (kJoinWarps * 32) > 0 ? kOwnTile * LPR / (kJoinWarps * 32) : 1;
+  constexpr int kLoads = kOwnTile * LPR / (WARPS * 32) > 0 ? kOwnTile * LPR / (WARPS * 32) : 1;
   __shared__ uint4 own[2][kOwnTile][LPR];              // K, V
   pdl_launch_dependents();
   pdl_wait();
@@ -1079,7 +1080,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
   const int head = in_req / a.p.chunks, chunk = in_req - head * a.p.chunks;
   const int2 by = a.held_by[pair];
   const Request rq = request_of(a, a.words[b]);
-  const int rows = min(a.p.rc, rq.n * a.grp - chunk * a.p.rc), r_cta = blockIdx.y * join_rows(HD);
+  const int rows = min(a.p.rc, rq.n * a.grp - chunk * a.p.rc), r_cta = blockIdx.y * join_rows(HD, WARPS);
   if (r_cta >= rows) return;
   // CTAs that hold tiles of these rows (within the grid even if one gave up before it left its number)
   const int c0 = rq.tiles > 0 ? max(by.x, 0) : 0, c1 = rq.tiles > 0 ? min(by.y, a.grid - 1) : -1;
@@ -1093,7 +1094,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
   auto fetch = [&](int j) {
 #pragma unroll
     for (int u = 0; u < kLoads; u++) {
-      const int at = threadIdx.x + u * kJoinWarps * 32, jr = at / LPR, c = at % LPR;
+      const int at = threadIdx.x + u * WARPS * 32, jr = at / LPR, c = at % LPR;
       kw[u] = vw[u] = make_uint4(0, 0, 0, 0);
       if (jr < kOwnTile && j + jr < n_own) {
         kw[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k_own) + (rq.row0 + j + jr) * a.ko_row + head * a.ko_head + c * 8);
@@ -1155,7 +1156,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
     }
 #pragma unroll
     for (int u = 0; u < kLoads; u++) {
-      const int at = threadIdx.x + u * kJoinWarps * 32;
+      const int at = threadIdx.x + u * WARPS * 32;
       if (at < kOwnTile * LPR) {
         own[0][at / LPR][at % LPR] = kw[u];
         own[1][at / LPR][at % LPR] = vw[u];
@@ -1218,6 +1219,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_attn_join_kernel(const 
   *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * a.o_row + qh * a.o_head + sub * 8) = w;
 }
 
+template <typename T, int HD, int WARPS>
+cudaError_t launch_join(const CacheAttnArgs& a, cudaStream_t s) {
+  const dim3 grid(a.n_req * a.n_kv * a.p.chunks, (a.p.rc + join_rows(HD, WARPS) - 1) / join_rows(HD, WARPS));
+  const bool many = a.grid >= 4 * (int)grid.x;         // pieces of a row: about the CTAs per (request, KV head, chunk)
+  return launch_pdl(many ? cache_attn_join_kernel<T, HD, WARPS, 8> : cache_attn_join_kernel<T, HD, WARPS, 4>, grid, dim3(WARPS * 32), 0, s, a);
+}
+
 template <typename T, int HD, int RP>
 cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
   static std::atomic<int> smem_set[kMaxDevices];
@@ -1232,9 +1240,7 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUtens
   }
   e = launch_pdl(cache_attn_kernel<T, HD, RP>, dim3(a.grid), dim3(kThreads), a.p.smem, s, a, kmap, vmap);
   if (e != cudaSuccess) return e;
-  const dim3 join_grid(a.n_req * a.n_kv * a.p.chunks, (a.p.rc + join_rows(HD) - 1) / join_rows(HD));
-  const bool many = a.grid >= 6 * (int)join_grid.x;    // pieces of a row: about the CTAs per (request, KV head, chunk)
-  return launch_pdl(many ? cache_attn_join_kernel<T, HD, 8> : cache_attn_join_kernel<T, HD, 4>, join_grid, dim3(kJoinWarps * 32), 0, s, a);
+  return a.p.rc <= join_rows(HD, 4) ? launch_join<T, HD, 4>(a, s) : launch_join<T, HD, 8>(a, s);
 }
 
 template <typename T, int HD>
