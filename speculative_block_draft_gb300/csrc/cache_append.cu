@@ -14,7 +14,7 @@
 //    amax and the rounding, so they are read once, and the next head's are on their way meanwhile;
 //  * at most kShortRun rows (rounds): a warp per run and head, latency-bound.
 // Measured, 5 layers x 8 heads x 128 columns of bf16: 128 rows in 2 runs 4.4 us together, 16.5 us by warps; 512
-// rows in 64 runs 33.9 us together, 7.0 us by warps. 16384 rows: 97 us, 5.2 TB/s read and written (the floor at the
+// rows in 64 runs 33.9 us together, 7.0 us by warps. 16384 rows: 94 us, 5.4 TB/s read and written (the floor at the
 // measured copy bandwidth is 74 us).
 #include <cuda_fp8.h>
 #include <math.h>
@@ -257,9 +257,11 @@ __device__ __forceinline__ void append_by_warp(const CacheAppendArgs& a, int row
   __syncwarp();   // owner belongs to the next run
 }
 
-// PER: eighths of a row per thread, block_tokens * head_dim / 8 / 256 (at least 1).
-template <typename T, int PER>
-__global__ void __launch_bounds__(kAppendThreads, PER * sizeof(T) <= 8 ? 4 : 1)
+// PER: eighths of a row per thread, block_tokens * head_dim / 8 / 256 (at least 1). CTAS per SM: five for prompts, for
+// the loads in flight (16384 rows: 93.8 us, 98.0 with four, 118.6 with six, which spills); four for rounds, which the
+// fewer registers slow (32 requests x 4-5 rows: 5.9 us, 6.8 with five).
+template <typename T, int PER, int CTAS>
+__global__ void __launch_bounds__(kAppendThreads, PER * sizeof(T) <= 8 ? CTAS : 1)
     cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
   __shared__ int owners[kAppendThreads / 32][128];   // last row of the call for each token of the block, -1: none
   int* owner = owners[0];
@@ -372,6 +374,19 @@ __global__ void __launch_bounds__(kAppendThreads, PER * sizeof(T) <= 8 ? 4 : 1)
   }
 }
 
+template <typename T, int CTAS>
+cudaError_t launch_per(const CacheAppendArgs& a, dim3 grid, cudaStream_t s) {
+  const dim3 block(kAppendThreads);
+  switch (((a.hd / 8) << a.log_t) / kAppendThreads) {
+    case 0: case 1: return launch_pdl(cache_append_kernel<T, 1, CTAS>, grid, block, 0, s, a);
+    case 2: return launch_pdl(cache_append_kernel<T, 2, CTAS>, grid, block, 0, s, a);
+    case 4: return launch_pdl(cache_append_kernel<T, 4, CTAS>, grid, block, 0, s, a);
+    case 8: return launch_pdl(cache_append_kernel<T, 8, CTAS>, grid, block, 0, s, a);
+    case 16: return launch_pdl(cache_append_kernel<T, 16, CTAS>, grid, block, 0, s, a);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 template <typename T>
 cudaError_t launch_rows(CacheAppendArgs a, cudaStream_t s) {
   // Heads per CTA: as many as leave several CTAs for every SM; with more, a CTA has loads on their way while it rounds.
@@ -385,15 +400,8 @@ cudaError_t launch_rows(CacheAppendArgs a, cudaStream_t s) {
   a.rows_per_cta = 8;
   while (a.rows_per_cta < std::max(64, 1 << a.log_t) && per_row * a.n_rows > 608LL * a.rows_per_cta) a.rows_per_cta *= 2;
   const long long row_ctas = (a.n_rows + a.rows_per_cta - 1) / a.rows_per_cta;
-  const dim3 grid((unsigned)row_ctas, 2 * ((a.n_kv + a.heads - 1) / a.heads), a.n_layers), block(kAppendThreads);
-  switch (((a.hd / 8) << a.log_t) / kAppendThreads) {
-    case 0: case 1: return launch_pdl(cache_append_kernel<T, 1>, grid, block, 0, s, a);
-    case 2: return launch_pdl(cache_append_kernel<T, 2>, grid, block, 0, s, a);
-    case 4: return launch_pdl(cache_append_kernel<T, 4>, grid, block, 0, s, a);
-    case 8: return launch_pdl(cache_append_kernel<T, 8>, grid, block, 0, s, a);
-    case 16: return launch_pdl(cache_append_kernel<T, 16>, grid, block, 0, s, a);
-    default: return cudaErrorInvalidValue;
-  }
+  const dim3 grid((unsigned)row_ctas, 2 * ((a.n_kv + a.heads - 1) / a.heads), a.n_layers);
+  return a.rows_per_cta >= std::max(64, 1 << a.log_t) ? launch_per<T, 5>(a, grid, s) : launch_per<T, 4>(a, grid, s);
 }
 
 }  // namespace
