@@ -259,7 +259,7 @@ __device__ __forceinline__ void append_by_warp(const CacheAppendArgs& a, int row
 
 // PER: eighths of a row per thread, block_tokens * head_dim / 8 / 256 (at least 1). CTAS per SM: five for prompts, for
 // the loads in flight (16384 rows: 93.8 us, 98.0 with four, 118.6 with six, which spills); four for rounds, which the
-// fewer registers slow (32 requests x 4-5 rows: 5.9 us, 6.8 with five).
+// fewer registers slow (32 requests x 1-8 rows: 5.9 us, 6.8 with five).
 template <typename T, int PER, int CTAS>
 __global__ void __launch_bounds__(kAppendThreads, PER * sizeof(T) <= 8 ? CTAS : 1)
     cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
