@@ -398,7 +398,7 @@ struct alignas(16) RowState {            // per query row of the CTA's chunk
   float qs[2][kRowArrays];               // the row's query scale; by turns for the segments, as the queries
   float f[kRowArrays], by[kRowArrays];   // factor of a moved reference, minus its step; 1 / L at the end
   float red[4][kRowArrays];              // per softmax warp: maxima, sums
-  uint32_t high[4];                      // per softmax warp: chunks of rows with a value above kMax
+  uint32_t moved[2];                     // rows 0-31, 32-63 whose reference moved
   int unset[kRowArrays];                 // the row has seen no key (its reference is 0)
   int64_t out[kRowArrays];               // its element offset in the output
 };
@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
         __syncwarp();
         // x = t - m of this key for each row
         float2 x[CH * 4];
-        uint32_t high = 0;                               // chunks of rows with an x above kMax
+        bool high = false;                               // an x above kMax
         const uint32_t ts = tmem + lanes + (uint32_t)((gg & 1) * NS);
         uint32_t s8[CH][8];
 #pragma unroll
@@ -867,10 +867,10 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
             x[ch * 4 + j] = v;
             top = fmaxf(top, fmaxf(v.x, v.y));
           }
-          if (top > kMax) high |= 1u << ch;
+          high |= top > kMax;
         }
         if (edge) {
-          high = 0;
+          high = false;
           const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
           for (int r = 0; r < CH * 4; r++) {
@@ -878,45 +878,38 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
             if (v_nan) x[r] = make_float2(nan, nan);
             if (!(two & 1)) x[r].x = -INFINITY;
             if (!(two & 2)) x[r].y = -INFINITY;
-            if (fmaxf(x[r].x, x[r].y) > kMax) high |= 1u << (r / 4);
+            high |= fmaxf(x[r].x, x[r].y) > kMax;
           }
         }
         // the probabilities of the tile before have been read, and its part of O is there
         if (gg > 0) wait(p_free, gg - 1);
-        const bool move = softmax_any(high != 0 || unset_any);
+        const bool move = softmax_any(high || unset_any);
         gone = dead[look++ & 1];
         if (gone) break;
         if (move) {
-          // New references: in the chunks of rows where some row passed 2^kMax, or all while a row has seen no key, the
-          // largest x of a row over the tile goes to kTop where it passed kMax or is the row's first.
-          high = __reduce_or_sync(0xffffffffu, high);
-          if (lane == 0) rs.high[quarter] = high;
-          softmax_sync();
-          high = unset_any ? (1u << CH) - 1 : rs.high[0] | rs.high[1] | rs.high[2] | rs.high[3];
+          // New references: the largest x of a row over the tile goes to kTop where it passed kMax or is the row's first.
+          // All rows are reduced, without branches between the chunks: their shuffles overlap.
 #pragma unroll
           for (int ch = 0; ch < CH; ch++) {
-            if ((high >> ch) & 1) {
-              const float v8[8] = {x[4 * ch].x, x[4 * ch].y, x[4 * ch + 1].x, x[4 * ch + 1].y, x[4 * ch + 2].x, x[4 * ch + 2].y, x[4 * ch + 3].x, x[4 * ch + 3].y};
-              const float mx = reduce8(v8, [](float p, float q) { return fmaxf(p, q); });
-              if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = mx;
-            }
+            const float v8[8] = {x[4 * ch].x, x[4 * ch].y, x[4 * ch + 1].x, x[4 * ch + 1].y, x[4 * ch + 2].x, x[4 * ch + 2].y, x[4 * ch + 3].x, x[4 * ch + 3].y};
+            const float mx = reduce8(v8, [](float p, float q) { return fmaxf(p, q); });
+            if ((lane & 3) == 0) rs.red[quarter][ch * 8 + (lane >> 2)] = mx;
           }
           softmax_sync();
           bool still = false;
+          float by = 0.f;                                // the reference grows by this
           if (key < RP) {
-            float by = 0.f;                              // the reference grows by this
-            bool first = false;
-            if ((high >> (key >> 3)) & 1) {
-              const float mx = fmaxf(fmaxf(rs.red[0][key], rs.red[1][key]), fmaxf(rs.red[2][key], rs.red[3][key]));
-              first = rs.unset[key] && mx > -INFINITY;
-              if (first || mx > kMax) by = mx - kTop;
-            }
+            const float mx = fmaxf(fmaxf(rs.red[0][key], rs.red[1][key]), fmaxf(rs.red[2][key], rs.red[3][key]));
+            const bool first = rs.unset[key] && mx > -INFINITY;
+            if (first || mx > kMax) by = mx - kTop;
             rs.f[key] = first ? 0.f : ex2(-by);
             rs.by[key] = -by;
             rs.neg_m[key] -= by;
             if (first) rs.unset[key] = 0;
             still = rs.unset[key];
           }
+          const uint32_t moved = __ballot_sync(0xffffffffu, by != 0.f);
+          if (lane == 0 && quarter < 2) rs.moved[quarter] = moved;
           unset_any = softmax_any(still);
 #pragma unroll
           for (int r = 0; r < CH * 4; r++) {
@@ -926,8 +919,8 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
           if (t > 0) {
             tc05_fence_after();
 #pragma unroll 1
-            for (uint32_t left = high; left; left &= left - 1) {
-              const int r0 = 8 * (__ffs(left) - 1);
+            for (int r0 = 0; r0 < RP; r0 += 8) {
+              if (!((rs.moved[r0 >> 5] >> (r0 & 31)) & 0xffu)) continue;
 #pragma unroll 1
               for (int p = 0; p < PANELS; p++) {
                 const uint32_t to = tmem_o + lanes + (uint32_t)(p * N + r0 * TERMS);
@@ -946,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
             }
             tmem_wait_st();
           }
-          softmax_sync();                                // f, by and high have been read
+          softmax_sync();                                // f, by and moved have been read
         }
         __syncwarp();
 #pragma unroll
