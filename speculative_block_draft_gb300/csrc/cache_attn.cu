@@ -750,20 +750,20 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
         umma_commit_warp(smem_u32(drained));
         wait_bar(drained, 0, nullptr);
       }
-  } else {
-    // ---- queries of the later segments, while the one before is at work ---------------------------------------
-    bool ok = true;
+    } else {
+      // ---- queries of the later segments, while the one before is at work ---------------------------------------
+      bool ok = true;
 #pragma unroll 1
-    for (int k = 0; ok && walk.next(a, before, words, sg); k++) {
-      if (k == 0) continue;
-      if (k >= 2) ok = wait_bar_warp(&q_free[k & 1], (k >> 1) + 1, a.err);
-      if (!ok) break;
-      prepare_queries<T, HD, TERMS, RP>(a, sg, q_s + (k & 1) * q_bytes, rs.qs[k & 1], threadIdx.x - 64, 64);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&q_full[k & 1]));
+      for (int k = 0; ok && walk.next(a, before, words, sg); k++) {
+        if (k == 0) continue;
+        if (k >= 2) ok = wait_bar_warp(&q_free[k & 1], (k >> 1) + 1, a.err);
+        if (!ok) break;
+        prepare_queries<T, HD, TERMS, RP>(a, sg, q_s + (k & 1) * q_bytes, rs.qs[k & 1], threadIdx.x - 64, 64);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&q_full[k & 1]));
+      }
     }
-  }
   } else {
     if (kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax ------------------------------------------------------------------------------------------
