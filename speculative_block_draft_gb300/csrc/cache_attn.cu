@@ -23,9 +23,10 @@
 // weight of 2^-2 and more; below, the subnormal codes' step of 2^-9 leaves at most 2 * 2^-10, which is 2^-14 of the
 // row's largest weight. (kTop = 3 moves less often, 42 us against 42.5 for 32 requests x 5 rows, and leaves 2^-12.)
 //
-// What bounds it: the cache's bytes, in the steady state (32 requests, 8 KV heads of 128 columns: 6.8 TB/s with 25
-// rows per KV head, 6.5 with 40, 6.0 with 45, from the difference of 16384 and 8192 keys each), and before it some
-// 12 us (one row) to 20 us (five) of start, first references, output and second kernel, which short contexts feel.
+// What bounds it: the cache's bytes, in the steady state (32 requests, 8 KV heads of 128 columns: 7.1 TB/s with 5
+// rows per KV head, 6.8 with 25 rows, 6.5 with 40, 5.6 with 45, from the difference of 16384 and 8192
+// keys each), and besides some 12 us (one row) to 18 us (25) of start, first references, output and second kernel,
+// which short contexts feel.
 //
 // Work is split by key tiles, not by requests: all tiles of all (request, KV head, row chunk) in one
 // line, an equal run of them for each CTA. A run may begin or end inside a (request, head, chunk); those
