@@ -25,7 +25,7 @@
 //
 // What bounds it: the cache's bytes, in the steady state (32 requests, 8 KV heads of 128 columns: 7.1 TB/s with 5
 // rows per KV head, 6.8 with 25 rows, 6.5 with 40, 5.6 with 45, from the difference of 16384 and 8192
-// keys each), and besides some 12 us (one row) to 18 us (25) of start, first references, output and second kernel,
+// keys each), and besides some 12 us (5 rows) to 18 us (25) of start, first references, output and second kernel,
 // which short contexts feel.
 //
 // Work is split by key tiles, not by requests: all tiles of all (request, KV head, row chunk) in one
