@@ -475,9 +475,11 @@ typedef struct {
 /* Rows that see no key get zeros. out may be q. Keys whose table entry is out of range are not seen, nor are those that
  * a ring no longer holds (before len - table_blocks * T). What masked keys' blocks hold does not matter; a
  * NaN in a value that some rows of a request see and others do not makes the whole output row of those
- * that see it NaN. Rounding: queries and probabilities enter the tensor
- * cores as sums of e4m3 values, 8 significant bits for bf16 rows and 11 for f16 rows (the format's own
- * precision); products accumulate in fp32, softmax sums and outputs are fp32 and rounded once. */
+ * that see it NaN. Rounding: queries enter the tensor
+ * cores with 8 significant bits for bf16 rows and 11 for f16 rows (the format's own precision) down to 2^-18 of the row's
+ * largest element, where they end; probabilities with 11 significant bits down to 2^-30 of the row's largest, where
+ * they end: a row over n keys loses at most n * 2^-30 of its largest weight, however the rest is spread. Products
+ * accumulate in fp32, softmax sums and outputs are fp32 and rounded once. */
 int dflash_cache_attention(dflash_cache* c, const dflash_attention* a, void* stream);
 
 /* The paged context cache of a handle made with cache_blocks > 0, for inspection and for moving contexts: its codes,

@@ -28,11 +28,9 @@ struct CacheAppendArgs {
 cudaError_t launch_cache_append(int dtype, const CacheAppendArgs& a, cudaStream_t s);
 
 // How a call's query rows are laid out over CTAs (plan_cache_attn): the grp * n rows of one request and
-// KV head are cut into chunks of rc rows, each padded to rp columns and carried as `terms` e4m3 terms.
+// KV head are cut into chunks of rc rows, each padded to rp columns.
 struct CacheAttnPlan {
-  int terms;               // e4m3 terms of a query or probability: 2 (bf16), 3 (f16)
   int chunks, rc, rp;
-  int ns, n;               // MMA columns: rp, and terms * rp, rounded up to 16 (n <= 128)
   int ctas_per_sm, stages, tmem_cols;
   int setup;               // tiles that the start and end of a chunk count for when the work is shared out
   size_t smem;

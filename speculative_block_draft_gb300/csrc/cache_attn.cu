@@ -10,18 +10,23 @@
 // Keys are the tensor-memory lanes of S, so a thread owns a key: few rows fill every lane, a row's
 // softmax needs no exchange between threads while its reference stays (below), and a thread's
 // probabilities are contiguous bytes of the second product's operand. Queries and probabilities
-// are not e4m3 values, so both enter as sums of e4m3 terms: a value's nearest code, the nearest code of what that
-// leaves, and so on. Two terms hold bf16's 8 significant bits, three f16's 11. The first product adds the
-// terms of Q up in one accumulator; those of P are further columns of the second one (cheaper: an MMA of up to
-// 64 columns takes the time of one of 64), added when O is read.
+// are not 8-bit values, so both enter as sums of 8-bit terms: a value's nearest code, the nearest code of what that
+// leaves, and so on. Queries are e4m3 terms of a row scaled to its largest element: two hold bf16's 8 significant
+// bits, three f16's 11, both down to a step of 2^-18 of that element. The first product adds them up in one accumulator.
+// Probabilities are three e5m2 terms (split8), which hold 11 significant bits over 30 powers of two. They are further
+// columns of the second product (cheaper: an MMA of up to 64 columns takes the time of one of 64), added when O is read.
 //
 //   t_ij = s_ij * q_scale_i * k_scale * scale * log2(e) + log2(v_scale)    (scales of the key's block)
 //   w_ij = 2^(t_ij - m_i)                       = p_ij * v_scale / 2^m_i
 //   O_i = sum_j w_ij * vcode_j,  L_i = sum_j w_ij / v_scale,  out_i = O_i / L_i
 // The reference m_i of a row is set so that its largest weight so far is 2^kTop, and moves only when a
-// weight would pass 2^kMax (kept below 448, the largest code): then L and O are rescaled. Two terms hold 8 bits of a
-// weight of 2^-2 and more; below, the subnormal codes' step of 2^-9 leaves at most 2 * 2^-10, which is 2^-14 of the
-// row's largest weight. (kTop = 3 moves less often, 42 us against 42.5 for 32 requests x 5 rows, and leaves 2^-12.)
+// weight would pass 2^kMax (kept below 57344, the largest code): then L and O are rescaled.
+// What the terms must hold: L counts a weight w in full and O counts its terms, so what is lost of the small weights adds
+// up over the keys, and rows with one large weight and very many small ones are the rule (the first token of a context, with
+// a small value). So the step at which a weight ends has to lie far below the largest weight over the number of keys.
+// It is 2^-20 (split8), half of it at most is lost: 2^-30 of the largest weight for each key, 2^-13 of it
+// over 2^17 keys. (Weights as two or three e4m3 terms, which end at 2^-9, lost the tail: 40% of a row over 16384 keys
+// of which one held 0.8.)
 //
 // What bounds it: the cache's bytes, in the steady state (32 requests, 8 KV heads of 128 columns: 7.1 TB/s with 5
 // rows per KV head, 6.8 with 25 rows, 6.5 with 40, 5.6 with 45, from the difference of 16384 and 8192
@@ -59,8 +64,10 @@ constexpr int kConstRing = 16;           // tiles whose key constants are kept
 // 89.7 us, 91.4 with six, 91.9 with three. Three for more rows, whose first tiles then come sooner: 4 requests x 8 rows
 // over 2000 to 9000 keys 26.5 us, 28.0 with four; with 256 columns (16 x 9 rows) 47.5 us, 47.0 with four.
 constexpr int kMaxStages = 4;
-constexpr int kPBytes = kTile * 128;     // probabilities: 128 keys x up to 128 columns
-constexpr float kTop = 5.f, kMax = 8.75f;
+constexpr int kPPanel = kTile * 128;     // probabilities: 128 keys x up to 128 columns a panel
+constexpr int kPTerms = 3;               // terms of a probability
+constexpr float kTop = 9.f, kMax = 15.5f;
+constexpr float kLast = 64.f;            // its last term is stored times this
 constexpr float kUnset = -1e30f;         // reference of a piece whose row has seen no key
 // Built for two CTAs per SM, with 128 registers per thread: 16 requests x 9 rows of 5 query heads, 128 columns, 71 us
 // with two CTAs and 90 us with one. With 256 columns shared memory holds one, and more registers help from 48 rows on
@@ -180,10 +187,11 @@ struct Walk {
 };
 
 // ---- tensor-core pieces --------------------------------------------------------------------------
-// kind::f8f6f4, e4m3 x e4m3 -> fp32; the major bits (15, 16) say that an operand's rows run along
-// the contraction (MN-major).
-__device__ __forceinline__ constexpr uint32_t idesc_e4m3(int n, bool mn_major) {
-  return (1u << 4) | (mn_major ? (3u << 15) : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+// kind::f8f6f4, M = 128, e4m3 x e4m3 (bits 10-12: the second operand's format, 0 = e4m3, 1 = e5m2) -> fp32
+__device__ __forceinline__ constexpr uint32_t idesc_scores(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (8u << 24); }
+// e4m3 x e5m2; the major bits (15, 16) say that the operands' rows run along the contraction (MN-major).
+__device__ __forceinline__ constexpr uint32_t idesc_weights(int n) {
+  return (1u << 4) | (1u << 10) | (3u << 15) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
 
 // Shared-memory descriptor: swizzle 2 = 128 B, 4 = 64 B; sbo: bytes between groups of 8 rows (keys or
@@ -193,7 +201,7 @@ __device__ __forceinline__ constexpr uint64_t smem_desc(uint32_t addr, uint32_t 
          ((uint64_t)swizzle << 61);
 }
 
-__device__ __forceinline__ void umma_e4m3_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void umma_f8_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\t"
@@ -363,33 +371,34 @@ __device__ __forceinline__ void split4(float2 x, float2 y, uint32_t (&c)[TERMS])
   }
 }
 
-// The nearest value of 4 significant bits (1 + 3, as e4m3 has) to x >= 0, halves up; a NaN becomes 0.
-__device__ __forceinline__ float four_bits(float x) { return __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xfff00000u); }
-
-// Eight weights (>= 0, <= 448) as TERMS groups of eight e4m3 codes. In fp32: the conversions from fp32 are single
-// instructions, and taking the four bits of a term off is exact. A weight below 2^-6 meets the step of the subnormal
-// codes, 2^-9, in more than one term: it is off by at most 2 * 2^-10.
-template <int TERMS>
-__device__ __forceinline__ void split8(const float2 (&w)[4], uint2 (&c)[TERMS]) {
-  float2 r[4] = {w[0], w[1], w[2], w[3]};
+// Eight weights w >= 0, <= 2^kMax, as three groups of eight e5m2 codes. e5m2 is the upper byte of f16: with h the f16 nearest to w,
+//   c0 = h to 3 significant bits, c1 = h - c0 to 3, c2 = 64 (h - c0 - c1) to 3
+// where adding 0x80 to an f16's bits and dropping the low byte rounds to the nearest (halves away from 0; the differences are
+// exact). Each term leaves at most a sixteenth of what the one before left, half a step of the first being an eighth of its
+// power of two, so c0 + c1 + c2 / 64 is h: all its 11 bits. Below 2^-14 an f16 and the first two codes have steps of
+// 2^-24 and 2^-16; then the last code, of up to 2^-17 times 64, ends the sum within 2^-21. A NaN stays one.
+__device__ __forceinline__ void split8(const float2 (&w)[4], uint2 (&c)[kPTerms]) {
+  uint32_t h[4];
 #pragma unroll
-  for (int t = 0; t < TERMS; t++) {
-    float2 h[4];
+  for (int i = 0; i < 4; i++) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(w[i].y), "f"(w[i].x));
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      h[i] = r[i];
-      if (t + 1 < TERMS) {
-        h[i] = make_float2(four_bits(r[i].x), four_bits(r[i].y));
-        r[i] = add2(r[i], make_float2(-h[i].x, -h[i].y));
-      }
-    }
-    asm("{.reg .b16 p, q;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 p, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 q, %4, %3;\n\tmov.b32 %0, {p, q};}"
-        : "=r"(c[t].x) : "f"(h[0].x), "f"(h[0].y), "f"(h[1].x), "f"(h[1].y));
-    asm("{.reg .b16 p, q;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 p, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 q, %4, %3;\n\tmov.b32 %0, {p, q};}"
-        : "=r"(c[t].y) : "f"(h[2].x), "f"(h[2].y), "f"(h[3].x), "f"(h[3].y));
+  for (int t = 0; t + 1 < kPTerms; t++) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) r[i] = h[i] + 0x00800080u;
+    c[t].x = __byte_perm(r[0], r[1], 0x7531);
+    c[t].y = __byte_perm(r[2], r[3], 0x7531);
+#pragma unroll
+    for (int i = 0; i < 4; i++) asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(r[i] & 0xff00ff00u));
   }
+  constexpr uint32_t kLast2 = 0x54005400u;             // kLast, twice
+  static_assert(kLast == 64.f, "as in kLast2");
+#pragma unroll
+  for (int i = 0; i < 4; i++) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(kLast2));
+  asm("{.reg .b16 p, q;\n\tcvt.rn.satfinite.e5m2x2.f16x2 p, %1;\n\tcvt.rn.satfinite.e5m2x2.f16x2 q, %2;\n\tmov.b32 %0, {p, q};}"
+      : "=r"(c[kPTerms - 1].x) : "r"(h[0]), "r"(h[1]));
+  asm("{.reg .b16 p, q;\n\tcvt.rn.satfinite.e5m2x2.f16x2 p, %1;\n\tcvt.rn.satfinite.e5m2x2.f16x2 q, %2;\n\tmov.b32 %0, {p, q};}"
+      : "=r"(c[kPTerms - 1].y) : "r"(h[2]), "r"(h[3]));
 }
 
 // ---- shared memory -----------------------------------------------------------------------------------
@@ -404,14 +413,16 @@ struct alignas(16) RowState {            // per query row of the CTA's chunk
   int64_t out[kRowArrays];               // its element offset in the output
 };
 
-// MMA columns of the scores and of the weights (multiples of 16)
+// MMA columns of the scores and of the weights (multiples of 16), and rows of the queries' terms
 __host__ __device__ constexpr int score_columns(int rp) { return (rp + 15) / 16 * 16; }
-__host__ __device__ constexpr int weight_columns(int terms, int rp) { return (terms * rp + 15) / 16 * 16; }
+__host__ __device__ constexpr int weight_columns(int rp) { return (kPTerms * rp + 15) / 16 * 16; }
+__host__ __device__ constexpr int weight_panels(int rp) { return weight_columns(rp) > 128 ? 2 : 1; }
+__host__ __device__ constexpr int query_rows(int terms, int rp) { return (terms * rp + 15) / 16 * 16; }
 __host__ __device__ constexpr int panels_of(int hd) { return hd == 256 ? 2 : 1; }
 __host__ __device__ constexpr int stage_bytes(int hd) { return kTile * hd; }
 
-__host__ __device__ inline size_t attn_fixed_smem(int hd, int n, int n_req) {
-  return (size_t)2 * n * 128 * panels_of(hd) + kPBytes + sizeof(RowState) + (2 * kMaxStages + 12) * 8 + 80 + 20 * (size_t)(n_req + 1);
+__host__ __device__ inline size_t attn_fixed_smem(int hd, int terms, int rp, int n_req) {
+  return (size_t)2 * query_rows(terms, rp) * 128 * panels_of(hd) + weight_panels(rp) * kPPanel + sizeof(RowState) + (2 * kMaxStages + 12) * 8 + 80 + 20 * (size_t)(n_req + 1);
 }
 
 // ---- the first kernel ----------------------------------------------------------------------------------
@@ -421,7 +432,7 @@ __host__ __device__ inline size_t attn_fixed_smem(int hd, int n, int n_req) {
 template <typename T, int HD, int TERMS, int RP>
 __device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Segment& sg, uint8_t* q_s, float* qs, int tid, int threads) {
   constexpr int kPerRow = HD / 8, kAhead = 5;          // lanes of a row; rows in flight per lane
-  constexpr int N = weight_columns(TERMS, RP);
+  constexpr int N = query_rows(TERMS, RP);
   const int r0 = sg.chunk * a.p.rc, rows = min(a.p.rc, sg.r.n * a.grp - r0);
   const int c8 = (tid % kPerRow) * 8, at_once = threads / kPerRow;
   if (tid < RP && tid >= rows) qs[tid] = 0.f;          // padding: whatever is there counts nothing
@@ -474,26 +485,26 @@ __device__ __forceinline__ void prepare_queries(const CacheAttnArgs& a, const Se
 
 // RP: query rows of a chunk, padded to the next of 8, 16, 24, 32, 40, 48 (bf16) and 64 (bf16). It is known here so that
 // the loops over the rows have no branches: with one, every eight rows would wait for their own loads (32 requests x 25
-// rows 81 us; 64 without, and with weights split in fp32). 25 rows padded to 40 instead of 32 take 53.1 us against 49.5, 45 rows to 64 instead of 48 100
+// rows 81 us; 64 without, and with weights split in two). 25 rows padded to 40 instead of 32 take 53.1 us against 49.5, 45 rows to 64 instead of 48 100
 // against 90.
 template <typename T, int HD, int RP>
 __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
     cache_attn_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
-  constexpr int TERMS = __is_same(T, __nv_bfloat16) ? 2 : 3;
+  constexpr int TERMS = __is_same(T, __nv_bfloat16) ? 2 : 3;   // of a query
   constexpr int PANELS = panels_of(HD), STAGE = stage_bytes(HD);
   constexpr int ROWB = HD < 128 ? HD : 128;            // bytes of a key in a panel
   constexpr int PANEL = kTile * 128;                   // bytes between panels (HD = 256)
   constexpr int CH = RP / 8;                           // chunks of 8 rows
-  constexpr int NS = score_columns(RP), N = weight_columns(TERMS, RP);
+  constexpr int NS = score_columns(RP), N = weight_columns(RP), NQ = query_rows(TERMS, RP);
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  constexpr int q_bytes = N * 128 * PANELS;
+  constexpr int q_bytes = NQ * 128 * PANELS;
   const int S = a.p.stages;
   uint8_t* ring = sm;
   uint8_t* q_s = ring + (size_t)S * STAGE;             // two buffers, by turns for the segments
   uint8_t* p_s = q_s + 2 * q_bytes;
-  RowState& rs = *reinterpret_cast<RowState*>(p_s + kPBytes);
+  RowState& rs = *reinterpret_cast<RowState*>(p_s + weight_panels(RP) * kPPanel);
   uint64_t* bars = reinterpret_cast<uint64_t*>(&rs + 1);
   uint64_t *full = bars, *empty = bars + kMaxStages, *s_full = bars + 2 * kMaxStages, *s_free = s_full + 2, *q_full = s_full + 4,
            *q_free = s_full + 6, *p_full = s_full + 8, *p_free = s_full + 9, *drained = s_full + 10, *q_first = s_full + 11;
@@ -687,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
       }
     } else if (warp == 1) {
       // ---- MMAs ---------------------------------------------------------------------------------------------
-      const uint32_t id_s = idesc_e4m3(NS, false), id_o = idesc_e4m3(N, true);
+      const uint32_t id_s = idesc_scores(NS);
       const uint32_t ring_a = smem_u32(ring);
       const uint64_t qd0 = smem_desc(smem_u32(q_s), 16, 1024, 2), pd = smem_desc(smem_u32(p_s), 16, 1024, 2);
       Ring at;                                           // consumed in the order of the copies
@@ -709,9 +720,9 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
 #pragma unroll
           for (int ks = 0; ks < HD / 32; ks++) {
             const uint64_t ka = kd + (uint64_t)((ks / 4) * (PANEL >> 4) + (ks % 4) * 2);
-            const uint64_t qa = qd + (uint64_t)((ks / 4) * (N * 8) + (ks % 4) * 2);
+            const uint64_t qa = qd + (uint64_t)((ks / 4) * (NQ * 8) + (ks % 4) * 2);
 #pragma unroll
-            for (int i = 0; i < TERMS; i++) umma_e4m3_warp(d, ka, qa + (uint64_t)(i * RP * 8), id_s, ks > 0 || i > 0);
+            for (int i = 0; i < TERMS; i++) umma_f8_warp(d, ka, qa + (uint64_t)(i * RP * 8), id_s, ks > 0 || i > 0);
           }
           umma_commit_warp(smem_u32(&empty[slot]));
           umma_commit_warp(smem_u32(&s_full[gg & 1]));
@@ -734,8 +745,10 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
           for (int p = 0; p < PANELS; p++)
 #pragma unroll
             for (int ks = 0; ks < 4; ks++)
-              umma_e4m3_warp(tmem_o + p * N, vd + (uint64_t)((p * PANEL + ks * 32 * ROWB) >> 4), pd + (uint64_t)((ks * 32 * 128) >> 4),
-                             id_o, t > 0 || ks > 0);
+#pragma unroll
+              for (int n0 = 0; n0 < N; n0 += 128)        // a panel of weights each
+                umma_f8_warp(tmem_o + p * N + n0, vd + (uint64_t)((p * PANEL + ks * 32 * ROWB) >> 4),
+                             pd + (uint64_t)((n0 / 128 * kPPanel + ks * 32 * 128) >> 4), idesc_weights(N - n0 < 128 ? N - n0 : 128), t > 0 || ks > 0);
           umma_commit_warp(smem_u32(&empty[slot]));
           umma_commit_warp(smem_u32(p_free));
           pv_done = gg + 1;
@@ -924,12 +937,12 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
               if (!((rs.moved[r0 >> 5] >> (r0 & 31)) & 0xffu)) continue;
 #pragma unroll 1
               for (int p = 0; p < PANELS; p++) {
-                const uint32_t to = tmem_o + lanes + (uint32_t)(p * N + r0 * TERMS);
-                uint32_t o8[TERMS][8];
+                const uint32_t to = tmem_o + lanes + (uint32_t)(p * N + r0 * kPTerms);
+                uint32_t o8[kPTerms][8];
 #pragma unroll
-                for (int i = 0; i < TERMS; i++) tmem_start8(to + i * 8, o8[i]);
+                for (int i = 0; i < kPTerms; i++) tmem_start8(to + i * 8, o8[i]);
 #pragma unroll
-                for (int i = 0; i < TERMS; i++) {
+                for (int i = 0; i < kPTerms; i++) {
                   tmem_wait8(o8[i]);
                   float o[8];
 #pragma unroll
@@ -951,21 +964,15 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
             w[j] = make_float2(ex2(x[ch * 4 + j].x), ex2(x[ch * 4 + j].y));
             l[ch * 4 + j] = fma2(w[j], inv2, l[ch * 4 + j]);
           }
-          // columns of the product: per chunk of rows, its terms side by side (with two terms one 16-byte piece)
-          uint2 c[TERMS];
-          split8<TERMS>(w, c);
-          if constexpr (TERMS == 2) {
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + (uint32_t)((ch ^ (key & 7)) << 4)), "r"(c[0].x),
-                         "r"(c[0].y), "r"(c[1].x), "r"(c[1].y)
-                         : "memory");
-          } else {
+          // columns of the product: per chunk of rows, its terms side by side
+          uint2 c[kPTerms];
+          split8(w, c);
 #pragma unroll
-            for (int i = 0; i < TERMS; i++) {
-              const int o = (ch * TERMS + i) * 8;
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(p_row + (uint32_t)((((o >> 4) ^ (key & 7)) << 4) + (o & 8))),
-                           "r"(c[i].x), "r"(c[i].y)
-                           : "memory");
-            }
+          for (int i = 0; i < kPTerms; i++) {
+            const int o = (ch * kPTerms + i) * 8;
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(p_row + (uint32_t)((o >> 7) * kPPanel + (((o >> 4 & 7) ^ (key & 7)) << 4) + (o & 8))),
+                         "r"(c[i].x), "r"(c[i].y)
+                         : "memory");
           }
         }
         fence_proxy_async();
@@ -1008,15 +1015,15 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
       for (int p = 0; p < PANELS; p++) {
 #pragma unroll 1
         for (int ch = 0; ch < rows; ch += 8) {
-          uint32_t part8[TERMS][8];
+          uint32_t part8[kPTerms][8];
           float o8[8];
 #pragma unroll
-          for (int i = 0; i < TERMS; i++) tmem_start8(tmem_o + lanes + (uint32_t)(p * N + ch * TERMS + i * 8), part8[i]);
+          for (int i = 0; i < kPTerms; i++) tmem_start8(tmem_o + lanes + (uint32_t)(p * N + ch * kPTerms + i * 8), part8[i]);
 #pragma unroll
-          for (int i = 0; i < TERMS; i++) {
+          for (int i = 0; i < kPTerms; i++) {
             tmem_wait8(part8[i]);
 #pragma unroll
-            for (int j = 0; j < 8; j++) o8[j] = i == 0 ? __uint_as_float(part8[i][j]) : o8[j] + __uint_as_float(part8[i][j]);
+            for (int j = 0; j < 8; j++) o8[j] = i == 0 ? __uint_as_float(part8[i][j]) : fmaf(__uint_as_float(part8[i][j]), i + 1 < kPTerms ? 1.f : 1.f / kLast, o8[j]);
           }
           if (key < HD) {
             const int left = rows - ch;
@@ -1268,29 +1275,28 @@ cudaError_t launch_hd(const CacheAttnArgs& a, const CUtensorMap& kmap, const CUt
 
 CacheAttnPlan plan_cache_attn(int dtype, int hd, int grp, int max_q, int n_req) {
   CacheAttnPlan p{};
-  p.terms = dtype == DFLASH_BF16 ? 2 : 3;
-  // at most 128 MMA columns of weights, a swizzled row: then two score buffers and the output fit tensor memory as well
+  const int terms = dtype == DFLASH_BF16 ? 2 : 3;
+  // so many that two score buffers and the output fit tensor memory, and two buffers of queries shared memory
   const int limit = dtype == DFLASH_BF16 ? 64 : 40, rows = grp * max_q;
   p.chunks = (rows + limit - 1) / limit;
   p.rc = (rows + p.chunks - 1) / p.chunks;
   p.rp = p.rc <= 8 ? 8 : p.rc <= 16 ? 16 : p.rc <= 24 ? 24 : p.rc <= 32 ? 32 : p.rc <= 40 ? 40 : p.rc <= 48 ? 48 : 64;   // the kernels there are
-  p.n = weight_columns(p.terms, p.rp);
-  p.ns = score_columns(p.rp);
-  const int cols = 2 * p.ns + panels_of(hd) * p.n;
+  const int cols = 2 * score_columns(p.rp) + panels_of(hd) * weight_columns(p.rp);
   p.tmem_cols = 32;
   while (p.tmem_cols < cols) p.tmem_cols *= 2;
-  const size_t fixed = attn_fixed_smem(hd, p.n, n_req) + 1024;
+  const size_t fixed = attn_fixed_smem(hd, terms, p.rp, n_req) + 1024;
   constexpr size_t kPerSm = 227 * 1024;
-  // two CTAs per SM where registers and tensor memory allow it and each can hold four key or value tiles (one: 72 us
+  // two CTAs per SM where registers and tensor memory allow it and each can hold its key and value tiles (one: 72 us
   // against 53 for 32 requests x 5 rows, 36.5 against 30 for 4 x 8)
   const size_t half = kPerSm / 2 - 1024;
   // 32 requests x 5 rows over 512 to 2048 keys: 50.0 us if it counts nothing, 47.1 as 2 tiles, 46.5 as 3, 46.2 as 4; 16 x 9
   // causal rows over 500 to 8192: 70.9, 57.5, 55.7, 55.6, with 256 columns 66.4, 54.9, 53.4, 47.7; one request's 264
   // tiles: 15.5 us up to 3, 17.7 as 4.
   p.setup = hd == 256 ? 4 : 3;
-  p.ctas_per_sm = two_per_sm(hd, p.rp) && p.tmem_cols <= 256 && fixed + 4 * (size_t)stage_bytes(hd) <= half ? 2 : 1;
+  const size_t stages = hd == 256 || p.rp == 8 ? kMaxStages : 3;
+  p.ctas_per_sm = two_per_sm(hd, p.rp) && p.tmem_cols <= 256 && fixed + stages * stage_bytes(hd) <= half ? 2 : 1;
   const size_t room = (p.ctas_per_sm == 2 ? half : kPerSm) - fixed;
-  p.stages = (int)std::min<size_t>(hd == 256 || p.rp == 8 ? kMaxStages : 3, room / stage_bytes(hd));
+  p.stages = (int)std::min<size_t>(stages, room / stage_bytes(hd));
   p.smem = fixed + (size_t)p.stages * stage_bytes(hd);
   return p;
 }
