@@ -353,7 +353,8 @@ void dflash_destroy(dflash_handle* h);
  * l * layer_stride + n * block_stride + h * head_stride + t * token_stride + c of k and of v; every
  * stride and both addresses are multiples of 16. Scales are [n_layers][n_blocks][n_kv_heads].
  * Position p of a request is token p % T of block table[request][(p / T) % table_blocks], T =
- * block_tokens; its slot is block * T + p % T. The modulo makes the table a ring (dflash_pool.ring). */
+ * block_tokens; its slot is block * T + p % T. The modulo makes the table a ring (dflash_pool.ring): a
+ * block of it that starts anew has a new scale, so what is left of the positions it held is lost. */
 typedef struct {
   void *k, *v;               /* codes, see above; owned by the caller, as the scales */
   float *k_scale, *v_scale;
@@ -403,8 +404,12 @@ typedef struct {
   int n_blocks;              /* entries of free_list */
   int table_rows, table_blocks;
   int ring;                  /* 0: a request holds at most table_blocks blocks. 1: it may grow without
-                                end, position p reusing the block of position p - table_blocks * T;
-                                for windowed attention table_blocks >= ceil(window / T) + 1 */
+                                end, position p reusing the block of position p - table_blocks * T.
+                                A window needs table_blocks >= ceil((window + n - 1) / T) + 1, n the most
+                                rows that a request appends in a call and then attends causally from, or gives
+                                back (dflash_pool_truncate); n = 1 where it does neither. Without a window a
+                                ring shows its whole blocks, and only while nothing is given back (a request
+                                that ends apart): rows that are gone have replaced others */
   int32_t* lens;             /* [table_rows] tokens each request has */
   int32_t* table;            /* [table_rows][table_blocks] */
   int32_t* free_list;        /* [n_blocks]: free_count[0] unused blocks, taken from the end */
@@ -473,12 +478,12 @@ typedef struct {
 } dflash_attention;
 
 /* Rows that see no key get zeros. out may be q. Keys whose table entry is out of range are not seen, nor are those that
- * a ring no longer holds (before len - table_blocks * T). What masked keys' blocks hold does not matter; a
+ * a ring no longer holds (before (ceil(len / T) - table_blocks) * T). What masked keys' blocks hold does not matter; a
  * NaN in a value that some rows of a request see and others do not makes the whole output row of those
  * that see it NaN. Rounding: queries enter the tensor
  * cores with 8 significant bits for bf16 rows and 11 for f16 rows (the format's own precision) down to 2^-18 of the row's
- * largest element, where they end; probabilities with 11 significant bits down to 2^-30 of the row's largest, where
- * they end: a row over n keys loses at most n * 2^-30 of its largest weight, however the rest is spread. Products
+ * largest element, where they end; probabilities, times their blocks' value scales, with 11 significant bits down to
+ * 2^-30 of the row's largest, where they end: n keys lose at most n * 2^-30 of it, however the rest is spread. Products
  * accumulate in fp32, softmax sums and outputs are fp32 and rounded once. */
 int dflash_cache_attention(dflash_cache* c, const dflash_attention* a, void* stream);
 

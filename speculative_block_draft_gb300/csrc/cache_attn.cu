@@ -97,7 +97,10 @@ struct Request {
 // First visible position of row i of the request, and one past its last (cached keys). Lengths end below 2^31 - 2^16,
 // so positions of rows fit 32 bits.
 __device__ __forceinline__ void row_range(const CacheAttnArgs& a, const Request& r, int i, int& lo, int& hi) {
-  lo = max(0, r.len - a.held);                          // a ring holds the last ones
+  // a ring holds its last blocks; the newest one, of however few tokens, has a scale of its own, so that what is left of
+  // the one it replaced does not count
+  const int T = 1 << a.log_t;
+  lo = max(0, ((r.len + T - 1) & -T) - a.held);
   hi = r.len;
   if (a.causal) {
     const int at = a.k_own ? r.len + i : r.len - r.n + i;
