@@ -477,14 +477,14 @@ typedef struct {
   float scale;
 } dflash_attention;
 
-/* Rows that see no key get zeros. out may be q. Keys whose table entry is out of range are not seen, nor are those that
- * a ring no longer holds (before (ceil(len / T) - table_blocks) * T). What masked keys' blocks hold does not matter; a
- * NaN in a value that some rows of a request see and others do not makes the whole output row of those
- * that see it NaN. Rounding: queries enter the tensor
- * cores with 8 significant bits for bf16 rows and 11 for f16 rows (the format's own precision) down to 2^-18 of the row's
- * largest element, where they end; probabilities, times their blocks' value scales, with 11 significant bits down to
- * 2^-30 of the row's largest, where they end: n keys lose at most n * 2^-30 of it, however the rest is spread. Products
- * accumulate in fp32, softmax sums and outputs are fp32 and rounded once. */
+/* Rows that see no key get zeros, others with a NaN or infinite query NaN. out may be q. Keys whose table entry is out of
+ * range are not seen, nor are those that a ring no longer holds (before (ceil(len / T) - table_blocks) * T). What masked
+ * keys' blocks hold does not matter; a NaN in a value that some rows of a request see and others do not makes
+ * the whole output row of those that see it NaN. Rounding: queries enter the tensor cores with 8 significant bits for bf16
+ * rows and 11 for f16 rows (the format's own precision) down to 2^-18 of the row's largest element, where they end;
+ * probabilities, times their blocks' value scales, with 11 significant bits down to 2^-30 of the row's largest, where
+ * they end: n keys lose at most n * 2^-30 of it, however the rest is spread. Products accumulate in fp32, softmax sums
+ * and outputs are fp32 and rounded once. */
 int dflash_cache_attention(dflash_cache* c, const dflash_attention* a, void* stream);
 
 /* The paged context cache of a handle made with cache_blocks > 0, for inspection and for moving contexts: its codes,

@@ -1008,7 +1008,8 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
       if (key < RP) {
         const float L = (rs.red[0][key] + rs.red[1][key]) + (rs.red[2][key] + rs.red[3][key]);
         rs.f[key] = L == 0.f ? 0.f : 1.f / L;
-        if (!direct) a.part_ml[slot * RP + key] = make_float2(rs.unset[key] ? kUnset : -rs.neg_m[key], L);
+        // a row whose scores were all NaN has no reference, but a sum that the second kernel has to see
+        if (!direct) a.part_ml[slot * RP + key] = make_float2(rs.unset[key] && L == 0.f ? kUnset : -rs.neg_m[key], L);
       }
       softmax_sync();
       tc05_fence_after();
@@ -1115,6 +1116,8 @@ __global__ void __launch_bounds__(WARPS * 32) cache_attn_join_kernel(const __gri
   if (n_own > 0) {
     fetch(0);
     unpack(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + row * a.q_row + qh * a.q_head + sub * 8), q);
+#pragma unroll
+    for (int x = 0; x < 8; x++) q[x] = fabsf(q[x]) <= 3.402823466e38f ? q[x] : __int_as_float(0x7fffffff);   // as in the first kernel
   }
   float m = -INFINITY, L = 0.f, o[8];
 #pragma unroll
