@@ -243,10 +243,11 @@ int dflash_check_errors(dflash_handle* h, void* stream);
  * a NULL handle, DFLASH_ECUDA on a CUDA error.
  *
  * dflash_debug_stall: in the next dflash_draft_block call only, CTA `cta` of every tensor-core
- * projection launch also waits on an mbarrier that no copy and no thread completes, so that wait
- * runs out after the limit and the launch gives up; the round's outputs are then undefined and
- * dflash_check_errors returns DFLASH_ETIMEOUT (clearing the error word and the split-K tickets
- * the launches left). cta < 0 disarms it. Host-only. Returns DFLASH_EINVAL for a NULL handle. */
+ * projection launch also waits on an mbarrier that no copy and no thread completes (and that CTA of
+ * the paged cache's attention gets no keys), so that wait runs out after the limit and the launch
+ * gives up; the round's outputs are then undefined and dflash_check_errors returns DFLASH_ETIMEOUT
+ * (clearing the error word and the split-K tickets the launches left). cta < 0 disarms it. Host-only.
+ * Returns DFLASH_EINVAL for a NULL handle. */
 int dflash_set_wait_limit(dflash_handle* h, unsigned limit_us, void* stream);
 int dflash_debug_stall(dflash_handle* h, int cta);
 
@@ -397,6 +398,13 @@ void dflash_cache_destroy(dflash_cache* c);
  * DFLASH_EBOUNDS (builds with DFL_DEBUG_CHECKS): a slot, block number or row index was out of range;
  * every build skips such rows and keys. */
 int dflash_cache_check_errors(dflash_cache* c, void* stream);
+
+/* As dflash_set_wait_limit and dflash_debug_stall, for the attention calls on this cache (test hooks; host-only). The limit (at
+ * most 4 s) is that of the calls made from now on. The stall: in the next dflash_cache_attention call that
+ * launches, CTA `cta` of its first kernel gets no keys, so its waits run out if it has any to wait for. A
+ * handle made with cache_blocks passes both on to its cache. */
+int dflash_cache_set_wait_limit(dflash_cache* c, unsigned limit_us);
+int dflash_cache_debug_stall(dflash_cache* c, int cta);
 
 /* Block tables over a pool of n_blocks blocks; plain host struct, all pointers device memory. */
 typedef struct {

@@ -157,7 +157,7 @@ SYMBOLS = ["dflash_workspace_bytes", "dflash_create", "dflash_project_ctx", "dfl
            "dflash_accept_kept", "dflash_rows_matmul_plan", "dflash_rows_matmul", "dflash_set_wait_limit",
            "dflash_debug_stall", "dflash_accept_histogram", "dflash_cache_workspace_bytes", "dflash_cache_create",
            "dflash_cache_destroy", "dflash_cache_check_errors", "dflash_pool_reserve", "dflash_pool_truncate",
-           "dflash_cache_append", "dflash_cache_attention", "dflash_ctx_cache"]
+           "dflash_cache_append", "dflash_cache_attention", "dflash_ctx_cache", "dflash_cache_set_wait_limit", "dflash_cache_debug_stall"]
 
 
 def lib():
@@ -220,6 +220,10 @@ def lib():
         L.dflash_cache_destroy.argtypes = [vp]
         L.dflash_cache_check_errors.restype = i32
         L.dflash_cache_check_errors.argtypes = [vp, vp]
+        L.dflash_cache_set_wait_limit.restype = i32
+        L.dflash_cache_set_wait_limit.argtypes = [vp, ctypes.c_uint]
+        L.dflash_cache_debug_stall.restype = i32
+        L.dflash_cache_debug_stall.argtypes = [vp, i32]
         L.dflash_pool_reserve.restype = i32
         L.dflash_pool_reserve.argtypes = [P(dflash_pool), i32, vp, vp, vp, i32, vp, vp, vp]
         L.dflash_pool_truncate.restype = i32

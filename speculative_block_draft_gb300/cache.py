@@ -172,6 +172,14 @@ class Cache:
     def check_errors(self, stream=None) -> int:
         return _check(lib().dflash_cache_check_errors(self.h, _raw_stream(stream, self.device)), "dflash_cache_check_errors")
 
+    def set_wait_limit(self, limit_us: int) -> int:
+        """Test hook: limit of the attention's bounded waits in microseconds (0: the 1 s default)."""
+        return _check(lib().dflash_cache_set_wait_limit(self.h, limit_us), "dflash_cache_set_wait_limit")
+
+    def debug_stall(self, cta: int) -> int:
+        """Test hook: CTA `cta` of the next attention call gets no keys (cta < 0 disarms)."""
+        return _check(lib().dflash_cache_debug_stall(self.h, cta), "dflash_cache_debug_stall")
+
     def close(self):
         if getattr(self, "h", None):
             lib().dflash_cache_destroy(self.h)

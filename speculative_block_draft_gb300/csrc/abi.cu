@@ -1337,6 +1337,7 @@ int dflash_draft_block(dflash_handle* h, int n_req, const int32_t* req_ids, cons
       ca.window = c.window;
       ca.scale = (float)(1.0 / sqrt((double)c.head_dim));
       if (i == 0) probe_begin(h, DFLASH_PROBE_ATTN, s);
+      dflash_cache_debug_stall(h->cache, h->stall_active - 1);
       h->launches += 2;
       if ((st = dflash_cache_attention(h->cache, &ca, stream))) return st;
       if (i == 0) probe_end(h, DFLASH_PROBE_ATTN, s);
@@ -1681,7 +1682,8 @@ int dflash_accept_histogram(dflash_handle* h, uint64_t* counts, int n_counts, vo
 
 int dflash_set_wait_limit(dflash_handle* h, unsigned limit_us, void* stream) {
   if (!h) return DFLASH_EINVAL;
-  return status_of(cudaMemcpyAsync(h->err + 1, &limit_us, 4, cudaMemcpyHostToDevice, static_cast<cudaStream_t>(stream)));
+  const int st = status_of(cudaMemcpyAsync(h->err + 1, &limit_us, 4, cudaMemcpyHostToDevice, static_cast<cudaStream_t>(stream)));
+  return st || !h->cache ? st : dflash_cache_set_wait_limit(h->cache, limit_us);
 }
 
 int dflash_debug_stall(dflash_handle* h, int cta) {

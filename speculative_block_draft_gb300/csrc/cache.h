@@ -12,6 +12,7 @@ inline bool block_tokens_ok(int t) { return t == 16 || t == 32 || t == 64 || t =
 constexpr int kMinScaleExp = -64;
 
 constexpr unsigned kErrTimeoutCache = 4u;
+constexpr unsigned kWaitNs = 1000000000u;   // default limit of the attention's waits
 
 struct CacheAppendArgs {
   uint8_t* codes[2];        // K, V
@@ -49,6 +50,8 @@ struct CacheAttnArgs {
   int64_t q_row, q_head, o_row, o_head, ko_row, ko_head, vo_row, vo_head;   // elements
   float scale_log2;                                // scale * log2(e)
   unsigned* err;
+  unsigned wait_ns;                                // limit of the waits
+  int stall;                                       // test hook: CTA stall - 1 gets no keys (0: none)
   CacheAttnPlan p;
   int grid;                                        // CTAs of the first kernel
   int4* words;                                     // [n_req] what the call says about each request (read_request)

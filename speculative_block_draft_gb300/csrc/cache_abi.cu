@@ -13,13 +13,15 @@ using namespace dfl;
 struct dflash_cache {
   dflash_cache_config cfg;
   int device = 0, log_t = 0;
-  unsigned* err = nullptr;      // [0] error bits, [1] wait limit in us (0: 1 s)
+  unsigned* err = nullptr;      // error bits
   int n_sm = 148;
   int4* requests = nullptr;     // [max_requests]
   int2* held_by = nullptr;      // [requests x KV heads x row chunks]
   float2* part_ml = nullptr;    // attention pieces: rows of (reference, sum), then of head_dim floats
   float* part_o = nullptr;
   int64_t part_rows = 0;
+  unsigned wait_ns = kWaitNs;
+  int stall = 0;                // the next attention call's CacheAttnArgs::stall
   CUtensorMap kmap{}, vmap{};
 };
 
@@ -165,6 +167,18 @@ int dflash_cache_check_errors(dflash_cache* c, void* stream) {
   return (word & kErrBounds) ? DFLASH_EBOUNDS : DFLASH_ETIMEOUT;
 }
 
+int dflash_cache_set_wait_limit(dflash_cache* c, unsigned limit_us) {
+  if (!c) return DFLASH_EINVAL;
+  c->wait_ns = limit_us ? std::min(limit_us, 4000000u) * 1000u : kWaitNs;
+  return DFLASH_OK;
+}
+
+int dflash_cache_debug_stall(dflash_cache* c, int cta) {
+  if (!c) return DFLASH_EINVAL;
+  c->stall = cta < 0 ? 0 : cta + 1;
+  return DFLASH_OK;
+}
+
 int dflash_cache_append(dflash_cache* c, int layer, int n_layers, int n_rows, const int32_t* slots,
                         const dflash_rows* k, const dflash_rows* v, int dtype, void* stream) {
   if (!c || !k || !v || n_rows < 0 || layer < 0 || n_layers < 0 || (int64_t)layer + n_layers > c->cfg.n_layers)
@@ -256,6 +270,7 @@ int dflash_cache_attention(dflash_cache* c, const dflash_attention* p, void* str
   a.vo_head = p->v_own.head_stride;
   a.scale_log2 = p->scale * 1.4426950408889634f;
   a.err = c->err;
+  a.wait_ns = c->wait_ns;
   a.p = plan_cache_attn(p->dtype, f.head_dim, a.grp, p->max_q, p->n_requests);
   // key tiles are counted in 32 bits: a request has at most as many as its table row names, and one more
   const int64_t pairs = (int64_t)p->n_requests * f.n_kv_heads * a.p.chunks;
@@ -267,6 +282,8 @@ int dflash_cache_attention(dflash_cache* c, const dflash_attention* p, void* str
   a.held_by = c->held_by;
   a.part_o = c->part_o;
   a.part_ml = c->part_ml;
+  a.stall = c->stall;
+  c->stall = 0;
   return status_of(launch_cache_attn(p->dtype, a, c->kmap, c->vmap, static_cast<cudaStream_t>(stream)));
 }
 
