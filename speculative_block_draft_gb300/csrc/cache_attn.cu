@@ -105,7 +105,7 @@ __device__ __forceinline__ void row_range(const CacheAttnArgs& a, const Request&
   if (a.causal) {
     const int at = a.k_own ? r.len + i : r.len - r.n + i;
     hi = min(hi, at + 1);
-    if (a.window > 0) lo = max(lo, at + 1 - a.window);
+    if (a.window > 0 && at >= a.window) lo = max(lo, at + 1 - a.window);   // a window may be as large as an int
   } else if (a.window > 0) {
     lo = max(lo, r.len - a.window);
   }
