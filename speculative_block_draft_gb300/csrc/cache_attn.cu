@@ -883,7 +883,8 @@ __global__ void __launch_bounds__(kThreads, two_per_sm(HD, RP) ? 2 : 1)
 #pragma unroll
           for (int j = 0; j < 4; j++) {
             const float2 sc = make_float2(__uint_as_float(s8[ch][2 * j]), __uint_as_float(s8[ch][2 * j + 1]));
-            const float2 v = fma2(mul2(sc, q2[j]), ka, add2(vb2, m2[j]));
+            // the scales first: their product with a sum may be finite where the query's alone is not
+            const float2 v = fma2(sc, mul2(q2[j], ka), add2(vb2, m2[j]));
             x[ch * 4 + j] = v;
             top = fmaxf(top, fmaxf(v.x, v.y));
           }

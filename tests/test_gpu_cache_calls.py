@@ -36,3 +36,19 @@ def test_largest_windows(window, own):
         want, tol = exact.attention(q[rows], kd, vd, dt, seen=seen[rows])
         got = out.cpu()
         assert torch.all((got[rows].double() - want).abs() <= tol) and not got[~rows].any()
+
+
+@pytest.mark.parametrize("power", [0, 60, 110, 118])
+def test_largest_queries(power):
+    """bf16 queries of up to 2^120 against keys and a scale as small: the scores are ordinary numbers."""
+    T, H, Hq, D, n, dt = 64, 1, 5, 128, 300, torch.bfloat16
+    k, v, ks, vs = ref.random_cache(1, 6, H, T, D, power)
+    ks.fill_(2.0 ** -6 if power == 0 else 2.0 ** -64)
+    scale = D ** -0.5 if power == 0 else D ** -0.5 * 2.0 ** (58 - power)
+    q = (torch.randn((3, Hq, D), generator=torch.Generator().manual_seed(1)) * 2.0 ** power).to(dt)
+    out = torch.zeros_like(q, device="cuda")
+    cache = pkg.Cache(k.cuda(), v.cuda(), ks.cuda(), vs.cuda(), max_requests=1, max_q=3, n_q_heads=Hq)
+    cache.attention(q.cuda(), ints([n]), ints([[4, 2, 0, 1, 5]]), out, scale=scale)
+    table = [4, 2, 0, 1, 5]
+    want, tol = exact.attention(q, exact.values(k[0], ks[0], table, n, T), exact.values(v[0], vs[0], table, n, T), dt, scale=scale)
+    assert torch.all((out.cpu().double() - want).abs() <= tol)
