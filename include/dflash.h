@@ -395,8 +395,8 @@ void dflash_cache_destroy(dflash_cache* c);
 
 /* As dflash_check_errors, for the calls on this cache: synchronises `stream`, reads and clears the
  * error word. DFLASH_ETIMEOUT: a bounded wait gave up, the outputs of that call are undefined.
- * DFLASH_EBOUNDS (builds with DFL_DEBUG_CHECKS): a slot, block number or row index was out of range;
- * every build skips such rows and keys. */
+ * DFLASH_EBOUNDS (builds with DFL_DEBUG_CHECKS): a slot, block number or row index was out of range, or a
+ * request of an attention call had more than max_q rows; every build skips such rows and keys. */
 int dflash_cache_check_errors(dflash_cache* c, void* stream);
 
 /* As dflash_set_wait_limit and dflash_debug_stall, for the attention calls on this cache (test hooks; host-only). The limit (at

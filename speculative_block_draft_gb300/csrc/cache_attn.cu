@@ -121,7 +121,8 @@ __device__ __forceinline__ int4 read_request(const CacheAttnArgs& a, int b) {
   const int req = a.requests ? a.requests[b] : b;
   if (a.row_start) {
     row0 = a.row_start[b];
-    n = min(a.row_start[b + 1] - row0, a.max_q);
+    n = a.row_start[b + 1] - row0;
+    if (!in_bounds(n <= a.max_q, a.err)) n = a.max_q;
   }
   const bool known = req >= 0 && req < a.table_rows;
   const int len = a.lens[known ? req : 0];
