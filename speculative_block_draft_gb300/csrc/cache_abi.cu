@@ -224,7 +224,7 @@ int dflash_cache_attention(dflash_cache* c, const dflash_attention* p, void* str
       (p->causal != 0 && p->causal != 1) || (p->dtype != DFLASH_BF16 && p->dtype != DFLASH_F16) ||
       !(p->scale == p->scale) || isinf(p->scale))
     return DFLASH_EINVAL;
-  if (p->n_requests == 0 || p->max_q == 0) return DFLASH_OK;
+  if (p->n_requests == 0 || p->max_q == 0 || p->n_rows == 0) return DFLASH_OK;
   if (p->n_requests > f.max_requests || p->max_q > f.max_q) return DFLASH_ECAPACITY;
   if (p->table_rows < 1 || p->table_blocks < 1 || !p->lens || !p->table) return DFLASH_EINVAL;
   if (!p->requests && p->n_requests > p->table_rows) return DFLASH_EINVAL;

@@ -52,3 +52,17 @@ def test_largest_queries(power):
     table = [4, 2, 0, 1, 5]
     want, tol = exact.attention(q, exact.values(k[0], ks[0], table, n, T), exact.values(v[0], vs[0], table, n, T), dt, scale=scale)
     assert torch.all((out.cpu().double() - want).abs() <= tol)
+
+
+def test_a_call_without_rows():
+    """A step in which no request has a row: nothing is done, whatever max_q and however many requests there are."""
+    k, v, ks, vs = (x.cuda() for x in ref.random_cache(1, 4, 2, 16, 64, 1))
+    cache = pkg.Cache(k, v, ks, vs, max_requests=3, max_q=4, n_q_heads=4)
+    q = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device="cuda")
+    own = torch.zeros((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    lens, table = ints([5, 6, 7]), ints([[0], [1], [2]])
+    assert cache.attention(q, lens, table, q.clone(), row_start=ints([0, 0, 0, 0]), causal=True) == 0
+    assert cache.attention(q, lens, table, q.clone(), row_start=ints([0, 0, 0, 0]), k_own=own, v_own=own) == 0
+    assert cache.attention(q, lens, table, q.clone()) == 0
+    assert cache.append(ints([]), own, own) == 0
+    assert cache.check_errors() == 0
