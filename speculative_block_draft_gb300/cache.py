@@ -45,14 +45,29 @@ def _rows(name, t, n, heads, head_dim, device, dtype):
     return t.data_ptr(), stride[0] if len(shape) == 4 else 0, stride[-3], stride[-2]
 
 
-def _raw_stream(stream, device):
-    """A cudaStream_t: the given stream's, or the one current on the tensors' device."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+class _OnStreams:
+    """Device memory of the object's own, and the streams that its calls ran on: PyTorch hands memory of a dropped object out again
+    once the work that was on them then is done. (Not for a stream given as a number, which may be gone by then:
+    whoever passes one keeps the object until its calls have run, as for calls captured into a graph.)"""
+
+    def _own(self, memory):
+        self._memory, self._streams = memory, {torch._C._cuda_getCurrentRawStream(memory.get_device())}
+
+    def _stream(self, stream) -> int:
+        """A cudaStream_t: the given stream's, or the one current on the tensors' device."""
+        if stream is None:
+            raw = torch._C._cuda_getCurrentRawStream(self.device)
+        elif hasattr(stream, "cuda_stream"):
+            raw = stream.cuda_stream
+        else:
+            return int(stream)
+        if raw not in self._streams:
+            self._memory.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+            self._streams.add(raw)
+        return raw
 
 
-class BlockPool:
+class BlockPool(_OnStreams):
     """Block tables over a pool of blocks of ``block_tokens`` tokens (dflash_pool_reserve and
     dflash_pool_truncate). Holds the calls' 256 bytes of device scratch; lens, table and the stack of
     free blocks are the caller's tensors:
@@ -68,6 +83,7 @@ class BlockPool:
         self.block_tokens, self.ring, self.max_requests = block_tokens, int(ring), max_requests
         self.scratch = torch.zeros(DFLASH_POOL_SCRATCH, dtype=torch.uint8, device=device)
         self.device = self.scratch.get_device()
+        self._own(self.scratch)
         self.p = dflash_pool()
         self._reserve, self._truncate = lib().dflash_pool_reserve, lib().dflash_pool_truncate
 
@@ -86,16 +102,16 @@ class BlockPool:
         return _check(self._reserve(self._pool(n, lens, table, free, free_count), n, _ints("requests", requests, n, d),
                                     _ints("n_new", n_new, n, d), _ints("slots", slots, None, d), slots.numel(),
                                     _ints("row_start", row_start, n + 1, d), _ints("granted", granted, n, d),
-                                    _raw_stream(stream, d)), "dflash_pool_reserve")
+                                    self._stream(stream)), "dflash_pool_reserve")
 
     def truncate(self, new_len, lens, table, free, free_count, requests=None, stream=None) -> int:
         """Shorten table row requests[i] to new_len[i] tokens and give the blocks behind them back."""
         n, d = new_len.numel(), self.device
         return _check(self._truncate(self._pool(n, lens, table, free, free_count), n, _ints("requests", requests, n, d),
-                                     _ints("new_len", new_len, n, d), _raw_stream(stream, d)), "dflash_pool_truncate")
+                                     _ints("new_len", new_len, n, d), self._stream(stream)), "dflash_pool_truncate")
 
 
-class Cache:
+class Cache(_OnStreams):
     """A dflash_cache over the caller's codes and scales.
 
     k, v: e4m3 codes (torch.float8_e4m3fn or uint8) [layers][blocks][KV heads][block tokens][head_dim], the same
@@ -124,9 +140,10 @@ class Cache:
         if not k.is_cuda or self.device != torch.cuda.current_device():
             raise ValueError(f"the codes are on {k.device}, not on the current CUDA device")
         self.workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=k.device)
+        self._own(self.workspace)
         base = (self.workspace.data_ptr() + 255) // 256 * 256
         h = ctypes.c_void_p()
-        _check(lib().dflash_cache_create(ctypes.byref(cfg), base, nbytes, _raw_stream(stream, self.device), ctypes.byref(h)),
+        _check(lib().dflash_cache_create(ctypes.byref(cfg), base, nbytes, self._stream(stream), ctypes.byref(h)),
                "dflash_cache_create")
         self.h = h
         self._k, self._v, self._a = dflash_rows(), dflash_rows(), dflash_attention()
@@ -141,7 +158,7 @@ class Cache:
         _ROWS.pack_into(self._k, 0, *_rows("k_rows", k_rows, n, self.heads, self.head_dim, d, dt))
         _ROWS.pack_into(self._v, 0, *_rows("v_rows", v_rows, n, self.heads, self.head_dim, d, dt))
         return _check(self._append(self.h, layer, k_rows.shape[0] if k_rows.dim() == 4 else 1, n, _ints("slots", slots, n, d),
-                                   ctypes.byref(self._k), ctypes.byref(self._v), _row_dtype(k_rows), _raw_stream(stream, d)),
+                                   ctypes.byref(self._k), ctypes.byref(self._v), _row_dtype(k_rows), self._stream(stream)),
                       "dflash_cache_append")
 
     def attention(self, q, lens, table, out, layer: int = 0, row_start=None, max_q: int | None = None, k_own=None, v_own=None,
@@ -167,10 +184,10 @@ class Cache:
                              _ints("row_start", row_start, n_req + 1, d), _row_dtype(q), *_rows("q", q, n_rows, self.n_q_heads, hd, d, dt),
                              *_rows("out", out, n_rows, self.n_q_heads, hd, d, dt), *_rows("k_own", k_own, n_rows, heads, hd, d, dt),
                              *_rows("v_own", v_own, n_rows, heads, hd, d, dt), causal, window, hd ** -0.5 if scale is None else scale)
-        return _check(self._attention(self.h, ctypes.byref(self._a), _raw_stream(stream, d)), "dflash_cache_attention")
+        return _check(self._attention(self.h, ctypes.byref(self._a), self._stream(stream)), "dflash_cache_attention")
 
     def check_errors(self, stream=None) -> int:
-        return _check(lib().dflash_cache_check_errors(self.h, _raw_stream(stream, self.device)), "dflash_cache_check_errors")
+        return _check(lib().dflash_cache_check_errors(self.h, self._stream(stream)), "dflash_cache_check_errors")
 
     def set_wait_limit(self, limit_us: int) -> int:
         """Test hook: limit of the attention's bounded waits in microseconds (0: the 1 s default)."""

@@ -66,3 +66,36 @@ def test_a_call_without_rows():
     assert cache.attention(q, lens, table, q.clone()) == 0
     assert cache.append(ints([]), own, own) == 0
     assert cache.check_errors() == 0
+
+
+def test_an_object_dropped_while_its_calls_run():
+    """Calls on a stream other than the object's: its memory is not given to others before they are done."""
+    T, H, Hq, D, n, dt = 64, 2, 10, 128, 3000, torch.bfloat16
+    k, v, ks, vs = ref.random_cache(1, 50, H, T, D, 1)
+    dev, table = [x.cuda() for x in (k, v, ks, vs)], ref.random_table([n], T, 50, 47, 2)
+    q = torch.randn((4, Hq, D), generator=torch.Generator().manual_seed(3)).to(dt)
+    qd, lens, td, out = q.cuda(), ints([n]), ints(table), torch.zeros((4, Hq, D), dtype=dt, device="cuda")
+    pool_state = {"lens": ints([0]), "table": ints([[-1, -1]]), "free": ints([0, 1, 2]), "free_count": ints([3])}
+    slots, start, granted, new = ints([7] * 40), ints([0, 0]), ints([0]), ints([40])
+    cache, pool = pkg.Cache(*dev, max_requests=1, max_q=4, n_q_heads=Hq), pkg.BlockPool(64)
+    sizes = [x.numel() for x in (cache.workspace, pool.scratch)]
+    taken = [x.data_ptr() for x in (cache.workspace, pool.scratch)]
+    side = torch.cuda.Stream()
+    cache.attention(qd, lens, td, out)                 # first launches load the kernels, which may wait for the device
+    pool.reserve(ints([0]), **pool_state, slots=slots, row_start=start, granted=granted)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1000)
+    out.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)                 # some 0.2 s
+        cache.attention(qd, lens, td, out)
+    pool.reserve(new, **pool_state, slots=slots, row_start=start, granted=granted, stream=side)
+    del cache, pool
+    assert not side.query(), "the calls were done too early to tell"
+    others = [torch.empty(m, dtype=torch.uint8, device="cuda") for m in sizes]
+    assert all(o.data_ptr() != p for o, p in zip(others, taken))
+    side.synchronize()
+    want, tol = exact.attention(q, exact.values(k[0], ks[0], table[0], n, T), exact.values(v[0], vs[0], table[0], n, T), dt)
+    assert torch.all((out.cpu().double() - want).abs() <= tol)
+    assert slots.tolist() == list(range(128, 168)) and granted.tolist() == [1]
