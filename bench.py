@@ -40,13 +40,17 @@ def round_params(cfg) -> dict:
     return p
 
 
+def ctx_kv_bytes(cfg) -> int:
+    """Bytes of a context K or V element that attention reads: the ring's fp32 or f16, or a code of the paged 8-bit cache."""
+    return 1 if getattr(cfg, "cache_blocks", 0) else 4 if cfg.adtype == "f32" else 2
+
+
 def round_bytes(cfg, ctx_lens) -> dict:
     bpp = BYTES_PER_PARAM[cfg.wdtype]
     b = {k: v * bpp for k, v in round_params(cfg).items()}
     kvd = cfg.n_kv_heads * cfg.head_dim
-    act = 4 if cfg.adtype == "f32" else 2
     keys = sum(min(int(P), cfg.window) if cfg.window else int(P) for P in ctx_lens)
-    b["kv"] = cfg.n_layers * keys * kvd * 2 * act
+    b["kv"] = cfg.n_layers * keys * kvd * 2 * ctx_kv_bytes(cfg)
     if cfg.markov_rank:   # W2 of the Markov head streamed once per draft, plus the W1 rows
         b["markov"] = cfg.n_draft * cfg.vocab * cfg.markov_rank * bpp + cfg.batch * cfg.n_draft * cfg.markov_rank * bpp
     b["total"] = sum(b.values())
@@ -137,7 +141,6 @@ def tc05_classes(cfg, ctx_rows_per_round) -> set:
 def probe_classes(cfg, ctx_lens, ctx_rows_per_round):
     bpp = BYTES_PER_PARAM[cfg.wdtype]
     qd, kvd = cfg.n_q_heads * cfg.head_dim, cfg.n_kv_heads * cfg.head_dim
-    act = 4 if cfg.adtype == "f32" else 2
     keys = sum(min(int(P), cfg.window) if cfg.window else int(P) for P in ctx_lens)
     L, d, I = cfg.n_layers, cfg.d, cfg.inter
     # context calls of more than 32 rows on the tcgen05 path: W_c and every layer's K/V once per
@@ -145,7 +148,7 @@ def probe_classes(cfg, ctx_lens, ctx_rows_per_round):
     chunks = ctx_calls(cfg, ctx_rows_per_round)[0]
     return [("lm_head", 0, 1, cfg.vocab * cfg.target_hidden * bpp),
             ("qkv", 1, L, (qd + 2 * kvd) * d * bpp),
-            ("attention", 2, L, keys * kvd * 2 * act),
+            ("attention", 2, L, keys * kvd * 2 * ctx_kv_bytes(cfg)),
             ("o", 3, L, d * qd * bpp),
             ("gate_up", 4, L, 2 * I * d * bpp),
             ("down", 5, L, d * I * bpp),
@@ -217,7 +220,7 @@ def class_rooflines(cfg, classes, class_ms, t_round_ms, peaks, ctx_lens, ctx_row
                      "peak_source": f"{peaks['source']} (cuBLAS bf16 burst, MEASURED_PEAKS.json bf16_tflops)"})
     else:
         roof.update({"achieved": dk["achieved_gbs"], "peak": peaks["hbm_gbs"], "unit": "GB/s",
-                     "frac": dk["frac"], "traffic": None if dom in tc else load_traffic(dom),
+                     "frac": dk["frac"], "traffic": None if dom in tc or (dom == "attention" and getattr(cfg, "cache_blocks", 0)) else load_traffic(dom),
                      "algorithmic_bytes_per_launch": dk["algorithmic_bytes_per_launch"],
                      "peak_source": f"{peaks['source']} (burst copy, MEASURED_PEAKS.json hbm_gbs)"})
     roof.update({"avg_launch_ms": dk["avg_launch_us"] / 1e3, "share_of_round": dk["share_of_round"]})
@@ -492,6 +495,7 @@ def workload_config(cfg) -> dict:
             "new_ctx_rows_per_round": list(cfg.appends()),
             **({"large_batch_tc05": True} if getattr(cfg, "large_batch_tc05", False) else {}),
             **({"skinny_tc05": True} if getattr(cfg, "skinny_tc05", False) else {}),
+            **({"cache_blocks": cfg.cache_blocks} if getattr(cfg, "cache_blocks", 0) else {}),
             "l2": "no flush: every round streams >1.4 GB of weights, far above the 129 MB L2"}
 
 
@@ -522,6 +526,8 @@ def main():
                     help="rounds per kernel class timed live after the timed region (one launch each)")
     ap.add_argument("--skinny-tc05", action="store_true",
                     help="draft calls of at most 32 block rows run their projections on the tcgen05 projection kernel")
+    ap.add_argument("--cache-blocks", type=int, default=0,
+                    help="library option: context K/V in a paged 8-bit cache of that many 64-token blocks")
     ap.add_argument("--profile-ctx", type=int, default=0,
                     help="prefill only this many context rows (for short profiler captures; not a bench value)")
     args = ap.parse_args()
@@ -539,6 +545,8 @@ def main():
         cfg = syn.with_overrides(cfg, large_batch_tc05=True)
     if args.skinny_tc05:
         cfg = syn.with_overrides(cfg, skinny_tc05=True)
+    if args.cache_blocks:
+        cfg = syn.with_overrides(cfg, cache_blocks=args.cache_blocks)
     if args.impl == "reference":
         return run_reference(args, cfg)
 
