@@ -73,6 +73,9 @@ class BlockPool(_OnStreams):
     free blocks are the caller's tensors:
 
       lens int32 [rows], table int32 [rows][blocks per request], free int32 [blocks], free_count int32 [1]
+
+    ring: requests may grow without end, and a window of w needs ceil((w + n - 1) / block_tokens) + 1 blocks per
+    request, n the most rows of a call that are attended causally or given back (dflash_pool.ring).
     """
 
     def __init__(self, block_tokens: int, max_requests: int | None = None, ring: bool = False, device="cuda"):

@@ -259,7 +259,9 @@ __device__ __forceinline__ void append_by_warp(const CacheAppendArgs& a, int row
 
 // PER: eighths of a row per thread, block_tokens * head_dim / 8 / 256 (at least 1). CTAS per SM: five for prompts, for
 // the loads in flight (16384 rows: 93.8 us, 98.0 with four, 118.6 with six, which spills); four for rounds, which the
-// fewer registers slow (32 requests x 1-8 rows: 5.9 us, 6.8 with five).
+// fewer registers slow (32 requests x 1-8 rows: 5.9 us, 6.8 with five). Measured on bf16 blocks of 64 x 128. In fp32 blocks of
+// up to 4096 elements spill at five (444 bytes: 16384 rows in blocks of 16 x 128 291.6 us for a floor of 123.8); above PER *
+// sizeof(T) = 8 a thread holds so much that one CTA fits an SM (8192 rows in blocks of 64 x 256 158.4 us for 74.2).
 template <typename T, int PER, int CTAS>
 __global__ void __launch_bounds__(kAppendThreads, PER * sizeof(T) <= 8 ? CTAS : 1)
     cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
