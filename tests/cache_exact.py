@@ -15,7 +15,7 @@ def values(codes, scales, table, length, T):
 def attention(q, k, v, dtype, scale=None, seen=None):
     """q [rows][Hq][D], k, v [H][n][D] in 64 bits, seen bool [rows][n] or None. The outputs and how far a call may be off,
     element by element:
-      u = eps / 2 of the result, its rounding to dtype;
+      u = eps / 2 of the result, its rounding to dtype; 2^-25 where it is below f16's normal range, whose step is 2^-24;
       2^-11 of each probability: it enters as a value of 11 significant bits;
       2^-30 of the row's largest one for each key: the step at which small ones end (half of 2^-20, the largest is kept at 2^9
       or more); 2^17 keys can add up 2^-13 of the largest value so, below u;
@@ -34,6 +34,6 @@ def attention(q, k, v, dtype, scale=None, seen=None):
     off = off + s.masked_fill(s == -torch.inf, 0).abs().amax(-1) * 2.0 ** -22
     o, reach = p @ v, p @ v.abs()
     tol = (u * o.abs() + (2.0 ** -11 + 2.0 ** -15 + 2 * off[..., None]) * reach
-           + 2.0 ** -30 * p.amax(-1, keepdim=True) * v.abs().sum(1, keepdim=True) + 2.0 ** -26)
+           + 2.0 ** -30 * p.amax(-1, keepdim=True) * v.abs().sum(1, keepdim=True) + 2.0 ** -25)
     back = lambda t: t.reshape(H, rows, Hq // H, D).permute(1, 0, 2, 3).reshape(rows, Hq, D)   # noqa: E731
     return back(o), back(tol)
